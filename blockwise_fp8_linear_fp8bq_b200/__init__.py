@@ -28,7 +28,8 @@ __all__ = [
     "quantize_group",
     "Operand",
     "row_operand", "block_operand", "mx_operand", "bf16_operand", "gemm", "gemm_workspace", "linear_forward",
-    "linear_dgrad", "linear_wgrad", "set_clock_counters", "check",
+    "linear_dgrad", "linear_wgrad", "embedding_forward", "embedding_backward", "layernorm_forward",
+    "layernorm_backward", "rmsnorm_backward", "grad_norm", "clip_grads", "set_clock_counters", "check",
 ]
 
 SCALE_FP32 = 0
@@ -80,6 +81,42 @@ class _CQuantJob(ctypes.Structure):
     ]
 
 
+class _CNormGrad(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("x", ctypes.c_void_p),
+        ("dres", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("M", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("lddy", ctypes.c_int64),
+        ("ldx", ctypes.c_int64),
+        ("lddres", ctypes.c_int64),
+        ("lddx", ctypes.c_int64),
+        ("gamma", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("dgamma", ctypes.c_void_p),
+        ("dbeta", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class _CGrad(ctypes.Structure):
+    _fields_ = [
+        ("g", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
 QUANT_KINDS = {"act": 0, "act_t": 1, "dual": 2, "weight": 3}
 
 
@@ -128,6 +165,27 @@ def lib():
         L.fp8bq_row_scale_ld.argtypes = [i64]
         L.fp8bq_scales_bytes.restype = i64
         L.fp8bq_scales_bytes.argtypes = [i32, i32, i64, i64]
+        u32, f32 = ctypes.c_uint32, ctypes.c_float
+        L.fp8bq_embedding_forward.restype = i32
+        L.fp8bq_embedding_forward.argtypes = [vp, i64, i64, i64, vp, i32, i64, f32, vp, i64, i32, i32, vp]
+        L.fp8bq_embedding_backward.restype = i32
+        L.fp8bq_embedding_backward.argtypes = [vp, i64, i64, i64, vp, i32, i64, f32, i64, vp, i64, i32, i32, u32, vp, i64,
+                                               vp]
+        L.fp8bq_embedding_workspace_bytes.restype = i64
+        L.fp8bq_embedding_workspace_bytes.argtypes = [i64, i64]
+        L.fp8bq_layernorm_forward.restype = i32
+        L.fp8bq_layernorm_forward.argtypes = [vp, i64, i64, i64, vp, vp, f32, vp, i64, vp, vp, i32, i32, vp]
+        for name in ("fp8bq_layernorm_backward", "fp8bq_rmsnorm_backward"):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = [ctypes.POINTER(_CNormGrad), vp]
+        L.fp8bq_norm_workspace_bytes.restype = i64
+        L.fp8bq_norm_workspace_bytes.argtypes = [i64, i64]
+        L.fp8bq_grad_norm.restype = i32
+        L.fp8bq_grad_norm.argtypes = [ctypes.POINTER(_CGrad), i32, vp, vp, i64, vp]
+        L.fp8bq_grad_clip.restype = i32
+        L.fp8bq_grad_clip.argtypes = [ctypes.POINTER(_CGrad), i32, ctypes.c_double, vp, vp, i64, vp]
+        L.fp8bq_grad_workspace_bytes.restype = i64
+        L.fp8bq_grad_workspace_bytes.argtypes = [i32]
         L.fp8bq_check.restype = i32
         L.fp8bq_check.argtypes = [vp]
         L.fp8bq_set_clock_counters.restype = i32
@@ -479,6 +537,249 @@ def linear_wgrad(dy: torch.Tensor, x: torch.Tensor, fmt: int = SCALE_FP32) -> to
     qdt, sdt = quantize_act_t(dy, fmt)
     qxt, sxt = quantize_act_t(x, fmt)
     return gemm(row_operand(qdt, sdt, fmt), row_operand(qxt, sxt, fmt))
+
+
+_ROW_DTYPES = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
+_ID_DTYPES = {torch.int32: 0, torch.int64: 1}
+
+
+def _row_dtype(t: torch.Tensor, name: str) -> int:
+    code = _ROW_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bf16, fp16 or fp32")
+    return code
+
+
+def _rows(t: torch.Tensor, name: str, shape=None, dtype=None, device=None) -> int:
+    """Checks a 2-D row-major CUDA tensor and gives its leading dimension."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D row-major tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not t.is_cuda:
+        raise ValueError("fp8bq runs on CUDA tensors only (no CPU path)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t: Optional[torch.Tensor], name: str, n: int, dtypes, device) -> Optional[int]:
+    """Checks an optional contiguous vector of n entries and gives its address."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries ({', '.join(map(str, dtypes))}) on {device}")
+    return t.data_ptr()
+
+
+def _run(device: torch.device, what: str, *args) -> None:
+    """Calls the library with `device` current, on its current stream."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _raise(getattr(lib(), what)(*args, stream), what)
+    else:
+        with torch.cuda.device(device):
+            _raise(getattr(lib(), what)(*args, stream), what)
+
+
+def _workspace_bytes(device: torch.device, what: str, *args) -> int:
+    if torch.cuda.current_device() == device.index:
+        n = getattr(lib(), what)(*args)
+    else:
+        with torch.cuda.device(device):
+            n = getattr(lib(), what)(*args)
+    if n < 0:
+        raise RuntimeError(f"{what}: bad arguments or no usable device")
+    return n
+
+
+def _ids(ids: torch.Tensor, device) -> int:
+    if ids.dtype not in _ID_DTYPES or not ids.is_contiguous() or ids.device != device:
+        raise ValueError(f"ids must be a contiguous int32 or int64 tensor on {device}")
+    return _ID_DTYPES[ids.dtype]
+
+
+def embedding_forward(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                      dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """scale * w[ids]: w [V, D] bf16, fp16 or fp32, ids int32 or int64 of any shape ->
+    [*ids.shape, D] in `dtype` (w's by default), or `out`, a row-major [ids.numel(), D].
+    An id outside [0, V) gives zeros and makes the next check() raise."""
+    code, ldw = _row_dtype(w, "w"), _rows(w, "w")
+    V, D = w.shape
+    wide, T = _ids(ids, w.device), ids.numel()
+    y = torch.empty((T, D), dtype=dtype or w.dtype, device=w.device) if out is None else out
+    ldy = _rows(y, "out", (T, D), dtype, w.device)
+    _run(w.device, "fp8bq_embedding_forward", w.data_ptr(), V, D, ldw, ids.data_ptr(), wide, T, float(scale),
+         y.data_ptr(), ldy, code, _row_dtype(y, "out"))
+    return y.view(*ids.shape, D) if out is None else y
+
+
+EMBEDDING_ACCUMULATE = 1
+
+
+def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
+                       padding_id: Optional[int] = None, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                       dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The gradient of embedding_forward's table: [vocab, D] in `dtype` (fp32 or dy's),
+    row v the sum of scale * dy over the tokens with id v, zeros where there is none.
+    dy is [*ids.shape, D] or [ids.numel(), D].  With accumulate=True the sums are added
+    into `out`.  Tokens with id padding_id add nothing; an id outside [0, vocab) adds
+    nothing and makes the next check() raise."""
+    T = ids.numel()
+    D = dy.shape[-1] if dy.dim() > 0 else 0
+    if dy.dim() != 2:
+        if tuple(dy.shape) != (*ids.shape, D) or not dy.is_contiguous():
+            raise ValueError("dy must be [ids.numel(), D], or contiguous [*ids.shape, D]")
+        dy = dy.view(T, D)
+    code, lddy = _row_dtype(dy, "dy"), _rows(dy, "dy", (T, D))
+    wide = _ids(ids, dy.device)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs the tensor to add into")
+        out = torch.empty((vocab, D), dtype=dtype, device=dy.device)
+    lddw = _rows(out, "out", (vocab, D), None, dy.device)
+    n = _workspace_bytes(dy.device, "fp8bq_embedding_workspace_bytes", T, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
+    _run(dy.device, "fp8bq_embedding_backward", dy.data_ptr(), T, D, lddy, ids.data_ptr(), wide, vocab, float(scale),
+         -1 if padding_id is None else padding_id, out.data_ptr(), lddw, code, _row_dtype(out, "out"),
+         EMBEDDING_ACCUMULATE if accumulate else 0, ws.data_ptr(), n)
+    return out
+
+
+def layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                      eps: float = 1e-5, out=None):
+    """x [M, N] bf16, fp16 or fp32, gamma and beta [N] (x's dtype or fp32, or None) ->
+    (y, mean, rstd): y = (x - mean) * rstd * gamma + beta in x's dtype, mean and rstd
+    fp32 [M].  `out` may pass (y, mean, rstd) to write into (y may be x)."""
+    code, ldx = _row_dtype(x, "x"), _rows(x, "x")
+    M, N = x.shape
+    dev = x.device
+    pdt = next((p.dtype for p in (gamma, beta) if p is not None), x.dtype)
+    allowed = (x.dtype, torch.float32)
+    g = _vector(gamma, "gamma", N, allowed, dev)
+    b = _vector(beta, "beta", N, (pdt,), dev)
+    o = list(out) if out is not None else [None] * 3
+    y = torch.empty((M, N), dtype=x.dtype, device=dev) if o[0] is None else o[0]
+    mean = torch.empty(M, dtype=torch.float32, device=dev) if o[1] is None else o[1]
+    rstd = torch.empty(M, dtype=torch.float32, device=dev) if o[2] is None else o[2]
+    _run(dev, "fp8bq_layernorm_forward", x.data_ptr(), M, N, ldx, g, b, float(eps), y.data_ptr(),
+         _rows(y, "y", (M, N), x.dtype, dev), _vector(mean, "mean", M, (torch.float32,), dev),
+         _vector(rstd, "rstd", M, (torch.float32,), dev), code, _ROW_DTYPES.get(pdt, 0))
+    return y, mean, rstd
+
+
+NORM_ACCUMULATE = 1
+NORM_RSTD_F64 = 2
+
+
+def _norm_backward(what, dy, x, mean, rstd, gamma, dres, params, out, accumulate):
+    code, ldx = _row_dtype(x, "x"), _rows(x, "x")
+    M, N = x.shape
+    dev, layernorm = x.device, what == "fp8bq_layernorm_backward"
+    lddy = _rows(dy, "dy", (M, N), x.dtype, dev)
+    lddres = _rows(dres, "dres", (M, N), x.dtype, dev) if dres is not None else 0
+    g = _vector(gamma, "gamma", N, (x.dtype, torch.float32), dev)
+    o = list(out) if out is not None else [None] * 3
+    dx = torch.empty((M, N), dtype=x.dtype, device=dev) if o[0] is None else o[0]
+    dgamma = dbeta = None
+    n, ws = 0, None
+    if params:
+        if accumulate and (o[1] is None or (layernorm and o[2] is None)):
+            raise ValueError("accumulate=True needs the tensors to add into")
+        dgamma = torch.empty(N, dtype=torch.float32, device=dev) if o[1] is None else o[1]
+        if layernorm:
+            dbeta = torch.empty(N, dtype=torch.float32, device=dev) if o[2] is None else o[2]
+        n = _workspace_bytes(dev, "fp8bq_norm_workspace_bytes", M, N)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    f32 = (torch.float32,)
+    args = _CNormGrad(dy.data_ptr(), x.data_ptr(), None if dres is None else dres.data_ptr(), dx.data_ptr(), M, N, lddy, ldx,
+                      lddres, _rows(dx, "dx", (M, N), x.dtype, dev), g,
+                      _vector(mean, "mean", M, f32, dev) if layernorm else None,
+                      _vector(rstd, "rstd", M, (torch.float32, torch.float64), dev),
+                      _vector(dgamma, "dgamma", N, f32, dev), _vector(dbeta, "dbeta", N, f32, dev),
+                      None if ws is None else ws.data_ptr(), n, code,
+                      code if gamma is None else _ROW_DTYPES[gamma.dtype],
+                      (NORM_ACCUMULATE if accumulate else 0) | (NORM_RSTD_F64 if rstd.dtype == torch.float64 else 0), 0)
+    _run(dev, what, ctypes.byref(args))
+    return dx, dgamma, dbeta
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                       gamma: Optional[torch.Tensor] = None, dres: Optional[torch.Tensor] = None, params: bool = True,
+                       out=None, accumulate: bool = False):
+    """The backward pass of layernorm_forward: (dx, dgamma, dbeta), dx in x's dtype with
+    `dres` (the residual stream's gradient) added, dgamma and dbeta fp32 [N] (None with
+    params=False).  `out` may pass (dx, dgamma, dbeta) to write into; dx may be dy, x or
+    dres.  With accumulate=True dgamma and dbeta are added to."""
+    return _norm_backward("fp8bq_layernorm_backward", dy, x, mean, rstd, gamma, dres, params, out, accumulate)
+
+
+def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                     dres: Optional[torch.Tensor] = None, params: bool = True, out=None, accumulate: bool = False):
+    """The backward pass of h = x * rstd * gamma, with the rstd that rmsnorm_quantize
+    returned (fp32, or float64 from exact=True): (dx, dgamma), as layernorm_backward's.
+    `out` may pass (dx, dgamma) to write into."""
+    if out is not None:
+        out = (*out, None)
+    return _norm_backward("fp8bq_rmsnorm_backward", dy, x, None, rstd, gamma, dres, params, out, accumulate)[:2]
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill one span of memory, in some order."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _grad_table(grads, out):
+    table = (_CGrad * max(1, len(grads)))()
+    dev = None
+    for i, g in enumerate(grads):
+        code = _row_dtype(g, "a gradient")
+        if dev is None:
+            dev = g.device
+        if not g.is_cuda or g.device != dev:
+            raise ValueError("the gradients must be on one CUDA device")
+        if not _dense(g):
+            raise ValueError("a gradient must fill one span of memory")
+        o = g if out is None else out[i]
+        if o is not g and (o.shape != g.shape or o.stride() != g.stride() or o.device != dev):
+            raise ValueError("each output must have its gradient's shape, strides and device")
+        table[i] = (g.data_ptr(), o.data_ptr(), g.numel(), code, _row_dtype(o, "an output"))
+    return table, dev
+
+
+def _grad_call(what, grads, out, *more):
+    if len(grads) == 0:
+        raise ValueError("no gradients")
+    if out is not None and len(out) != len(grads):
+        raise ValueError("as many outputs as gradients")
+    table, dev = _grad_table(grads, out)
+    n = _workspace_bytes(dev, "fp8bq_grad_workspace_bytes", len(grads))
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    _run(dev, what, table, len(grads), *more, norm.data_ptr(), ws.data_ptr(), n)
+    return norm
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The 2-norm over all values of a list of bf16, fp16 or fp32 gradients (fp32 scalar on
+    the device)."""
+    return _grad_call("fp8bq_grad_norm", grads, None)
+
+
+def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Scales a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or into the
+    list `out` (same shapes; bf16, fp16 or fp32 each), and returns their global norm before
+    clipping (fp32 scalar on the device)."""
+    return _grad_call("fp8bq_grad_clip", grads, out, float(max_norm))
 
 
 def set_clock_counters(counters: Optional[torch.Tensor]) -> None:

@@ -1,0 +1,498 @@
+// embedding.cu -- embedding lookup with scaling and its gradient.
+//
+//   forward   y[t, :] = scale * W[id[t], :]
+//   backward  dW[v, :] (+)= scale * sum over t with id[t] = v of dY[t, :]
+//
+// Both are bound by HBM.  The gradient is summed without floating-point
+// atomics, so equal inputs give equal bits: the tokens are sorted by id (a
+// stable radix sort by one thread-block cluster, while the other SMs write
+// the zero rows of the dense gradient), equal chunks of the sorted tokens are
+// summed run by run, and a run that spans chunks is joined from its chunks'
+// partial sums in order.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fp8bq {
+namespace {
+
+// Token t's id, or `none` where it is outside [0, V): recorded in the status
+// word, which fp8bq_check() reports.
+__device__ __forceinline__ int64_t load_id(const void* ids, bool i64, int64_t t) {
+  return i64 ? static_cast<const int64_t*>(ids)[t] : static_cast<const int32_t*>(ids)[t];
+}
+
+// ---------------------------------------------------------------- forward --
+struct LookupParams {
+  const void* w;
+  const void* ids;
+  void* y;
+  int* status;
+  int64_t V, T, ldw, ldy;
+  int D, pieces;  // a row is `pieces` pieces of 32 lanes x 4 packs
+  float scale;
+  bool i64;
+};
+
+// A warp copies a piece of a row: four packs a lane in flight.
+template <class W, class Y, int VEC>
+__global__ void __launch_bounds__(256) lookup_kernel(const LookupParams p) {
+  constexpr int kPacks = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t t = warp / p.pieces;
+  if (t >= p.T) return;
+  const int c0 = static_cast<int>(warp - t * p.pieces) * (32 * kPacks * VEC) + lane * VEC;
+  const int64_t id = load_id(p.ids, p.i64, t);
+  const bool ok = id >= 0 && id < p.V;
+  if (!ok && c0 == 0) atomicCAS(p.status, 0, kStatusIndex);
+  const W* w = static_cast<const W*>(p.w) + (ok ? id : 0) * p.ldw;
+  Y* y = static_cast<Y*>(p.y) + t * p.ldy;
+  Pack<W, VEC> v[kPacks];
+#pragma unroll
+  for (int j = 0; j < kPacks; ++j) {
+    const int c = c0 + j * 32 * VEC;
+    if (c < p.D && ok) load_pack(v[j], w + c);
+  }
+#pragma unroll
+  for (int j = 0; j < kPacks; ++j) {
+    const int c = c0 + j * 32 * VEC;
+    if (c < p.D) {
+      Pack<Y, VEC> o;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o.v[i] = from_float<Y>(ok ? v[j].f(i) * p.scale : 0.0f);
+      store_pack(y + c, o);
+    }
+  }
+}
+
+template <class W, class Y>
+cudaError_t run_lookup(LookupParams p, cudaStream_t stream) {
+  constexpr int kVec = 16 / static_cast<int>(std::min(sizeof(W), sizeof(Y)));
+  const bool wide = p.D % kVec == 0 && rows_aligned(p.w, p.ldw, sizeof(W), 16) && rows_aligned(p.y, p.ldy, sizeof(Y), 16);
+  const int piece = 128 * (wide ? kVec : 1);
+  p.pieces = (p.D + piece - 1) / piece;
+  const int64_t blocks = (p.T * p.pieces + 7) / 8;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (wide)
+    lookup_kernel<W, Y, kVec><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+  else
+    lookup_kernel<W, Y, 1><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <class W>
+cudaError_t lookup_to(const LookupParams& p, int out_dtype, cudaStream_t stream) {
+  switch (out_dtype) {
+    case FP8BQ_BF16: return run_lookup<W, __nv_bfloat16>(p, stream);
+    case FP8BQ_FP16: return run_lookup<W, __half>(p, stream);
+    default: return run_lookup<W, float>(p, stream);
+  }
+}
+
+// --------------------------------------------------------------- backward --
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9;
+constexpr int kBins = 1 << kDigitBits;
+constexpr int kSortCluster = 8;
+
+// A sorted token: its id (V: none of the table's rows) and its position.
+struct alignas(8) Token {
+  uint32_t id, pos;
+};
+
+struct SortParams {
+  const void* ids;
+  Token* buf[2];  // the passes alternate, the last one writes buf[0]
+  int* status;
+  int64_t T, V, padding;
+  int64_t per_warp;  // tokens a warp of the cluster owns, a multiple of 32
+  int passes, bits;  // digits of `bits` bits
+  int sorters;       // blocks of the cluster; the others write zeros
+  bool i64;
+  uint8_t* dw;  // dense gradient to zero, or NULL
+  int64_t row_bytes, ld_bytes;
+};
+
+// Zeros over [p, p + bytes), shared by `n` threads of which this is the t-th.
+__device__ __forceinline__ void zero_span(uint8_t* p, int64_t bytes, int64_t t, int64_t n) {
+  const int64_t head = min(static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), bytes);
+  const int64_t wide = (bytes - head) / 16, tail0 = head + wide * 16;
+  uint4* q = reinterpret_cast<uint4*>(p + head);
+  for (int64_t i = t; i < wide; i += n) __stcs(q + i, make_uint4(0, 0, 0, 0));
+  for (int64_t i = t * 2; i < head; i += n * 2) *reinterpret_cast<uint16_t*>(p + i) = 0;
+  for (int64_t i = tail0 + t * 2; i < bytes; i += n * 2) *reinterpret_cast<uint16_t*>(p + i) = 0;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Stable radix sort of the tokens by id, least significant digit first.
+// Every warp owns a contiguous run of tokens and ranks its tokens in order
+// (equal digits in a warp's 32 found by a match), so no digit's order depends
+// on timing.  Counts and ranks live in shared memory; the blocks of the
+// cluster read one another's digit counts there.
+__global__ void __launch_bounds__(kSortThreads) sort_zero_kernel(const SortParams p) {
+  extern __shared__ uint32_t count[];  // [kSortWarps][kBins]
+  __shared__ uint32_t total[kBins], base[kBins], scan[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x >= static_cast<unsigned>(p.sorters)) {
+    const int64_t n = static_cast<int64_t>(gridDim.x - p.sorters) * kSortThreads;
+    const int64_t t = static_cast<int64_t>(blockIdx.x - p.sorters) * kSortThreads + tid;
+    if (p.row_bytes == p.ld_bytes) {
+      zero_span(p.dw, p.V * p.row_bytes, t, n);
+    } else {
+      for (int64_t v = t / 32; v < p.V; v += n / 32) zero_span(p.dw + v * p.ld_bytes, p.row_bytes, lane, 32);
+    }
+    return;  // whole clusters: the sorters' cluster holds none of these blocks
+  }
+  const uint32_t rank = p.sorters > 1 ? cluster_ctarank() : 0;
+  uint32_t* mine = count + warp * kBins;
+  const int64_t begin = (static_cast<int64_t>(rank) * kSortWarps + warp) * p.per_warp;
+  const int64_t end = min(begin + p.per_warp, p.T);
+  const int bins = 1 << p.bits;
+
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    const Token* from = p.buf[(p.passes - pass) & 1];
+    Token* to = p.buf[(p.passes - 1 - pass) & 1];
+    auto read = [&](int64_t i) {
+      Token k;
+      if (pass == 0) {
+        const int64_t id = load_id(p.ids, p.i64, i);
+        const bool ok = id >= 0 && id < p.V;
+        if (!ok) atomicCAS(p.status, 0, kStatusIndex);
+        k.id = static_cast<uint32_t>(ok && id != p.padding ? id : p.V);
+        k.pos = static_cast<uint32_t>(i);
+      } else {
+        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(from + i));
+        k.id = w.x;
+        k.pos = w.y;
+      }
+      return k;
+    };
+    for (int b = lane; b < bins; b += 32) mine[b] = 0;
+    __syncwarp();
+    for (int64_t i0 = begin; i0 < end; i0 += 32) {
+      const bool live = i0 + lane < end;
+      const uint32_t d = live ? (read(i0 + lane).id >> shift) & (bins - 1) : bins;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (live && lane == __ffs(same) - 1) mine[d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // per digit: where each warp's tokens start within the block's
+    if (tid < bins) {
+      uint32_t run = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = count[w * kBins + tid];
+        count[w * kBins + tid] = run;
+        run += c;
+      }
+      total[tid] = run;
+    }
+    // and where the block's start in the whole array
+    uint32_t before = 0, all = 0;
+    if (p.sorters > 1) {
+      cluster_sync();
+      if (tid < bins) {
+#pragma unroll
+        for (uint32_t r = 0; r < kSortCluster; ++r) {
+          const uint32_t c = ld_shared_cluster_u32(mapa_shared(smem_u32(&total[tid]), r));
+          if (r < rank) before += c;
+          all += c;
+        }
+      }
+    } else if (tid < bins) {
+      all = total[tid];
+    }
+    uint32_t incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    if (tid < bins) {
+      uint32_t lower = 0;
+      for (int w = 0; w < warp; ++w) lower += scan[w];
+      base[tid] = lower + incl - all + before;
+    }
+    __syncthreads();
+    for (int64_t i0 = begin; i0 < end; i0 += 32) {
+      const bool live = i0 + lane < end;
+      Token k{};
+      if (live) k = read(i0 + lane);
+      const uint32_t d = live ? (k.id >> shift) & (bins - 1) : bins;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      uint32_t at = 0;
+      if (live) at = base[d] + mine[d] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (live && lane == __ffs(same) - 1) mine[d] += __popc(same);
+      __syncwarp();
+      if (live) __stcg(reinterpret_cast<uint2*>(to + at), make_uint2(k.id, k.pos));
+    }
+    // the next pass reads what the whole cluster wrote, and rewrites `total`
+    if (p.sorters > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
+}
+
+struct GradParams {
+  const Token* tokens;
+  const void* dy;
+  void* dw;
+  float* partial;  // [chunks][2][D]: a chunk's first run where it began before, its last where it goes on
+  int64_t T, V, lddy, lddw, chunks;
+  int D, chunk;   // tokens a chunk
+  int cols;       // threads across the columns of a block, a power of two
+  float scale;
+  bool accumulate;
+};
+
+template <class G, int VEC>
+__device__ __forceinline__ void write_row(const GradParams& p, int64_t row, int c, const float (&acc)[VEC]) {
+  G* dst = static_cast<G*>(p.dw) + row * p.lddw + c;
+  Pack<G, VEC> o;
+  if (p.accumulate) {
+    load_pack(o, dst);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o.v[i] = from_float<G>(fmaf(p.scale, acc[i], o.f(i)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o.v[i] = from_float<G>(p.scale * acc[i]);
+  }
+  store_pack(dst, o);
+}
+
+// One chunk of sorted tokens a thread group, VEC columns a thread: rows of dY
+// are fetched eight at a time and summed in order.
+template <class T, class G, int VEC>
+__global__ void __launch_bounds__(256) grad_chunk_kernel(const GradParams p) {
+  constexpr int kBatch = 8;
+  cudaGridDependencySynchronize();
+  const int tx = threadIdx.x & (p.cols - 1), ty = threadIdx.x / p.cols;
+  const int64_t chunk = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.cols) + ty;
+  const int c = (blockIdx.y * p.cols + tx) * VEC;
+  if (chunk >= p.chunks || c >= p.D) return;
+  const int64_t begin = chunk * p.chunk, end = min(begin + p.chunk, p.T);
+  const uint32_t none = static_cast<uint32_t>(p.V);
+  uint32_t cur = p.tokens[begin].id;
+  bool head = begin > 0 && p.tokens[begin - 1].id == cur;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  auto flush = [&](bool tail) {
+    if (cur == none) return;
+    if (head || tail) {
+      float* dst = p.partial + (chunk * 2 + (head ? 0 : 1)) * static_cast<int64_t>(p.D) + c;
+      Pack<float, VEC> o;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o.v[i] = acc[i];
+      store_pack(dst, o);
+    } else {
+      write_row<G, VEC>(p, cur, c, acc);
+    }
+  };
+  for (int64_t i0 = begin; i0 < end; i0 += kBatch) {
+    Token tok[kBatch];
+    Pack<T, VEC> v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) tok[k] = i0 + k < end ? p.tokens[i0 + k] : Token{none, 0};
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (tok[k].id != none) load_pack<true>(v[k], static_cast<const T*>(p.dy) + tok[k].pos * p.lddy + c);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k >= end) break;
+      if (tok[k].id != cur) {
+        flush(false);
+        cur = tok[k].id;
+        head = false;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+      }
+      if (cur != none) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] += v[k].f(i);
+      }
+    }
+  }
+  flush(end < p.T && p.tokens[end].id == cur);
+}
+
+// The runs that span chunks: the chunk where one begins adds the later
+// chunks' partial sums to its own, in order.
+template <class G, int VEC>
+__global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p) {
+  cudaGridDependencySynchronize();
+  const int64_t chunk = blockIdx.x, begin = chunk * p.chunk, end = min(begin + p.chunk, p.T);
+  if (end >= p.T) return;
+  const uint32_t cur = p.tokens[end - 1].id;
+  if (cur == static_cast<uint32_t>(p.V) || p.tokens[end].id != cur) return;
+  if (begin > 0 && p.tokens[begin - 1].id == cur) return;  // began earlier
+  // the last chunk that holds the run: chunk k does while its first token is in it
+  int64_t last = chunk + 1;
+  for (;;) {
+    const int64_t first = (last + 1 + (threadIdx.x & 31)) * p.chunk;
+    const unsigned in = __ballot_sync(0xffffffffu, first < p.T && p.tokens[min(first, p.T - 1)].id == cur);
+    const int more = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+    last += more;
+    if (more < 32) break;
+  }
+  for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC; c < p.D; c += gridDim.y * blockDim.x * VEC) {
+    const float* src = p.partial + c;
+    float acc[VEC];
+    Pack<float, VEC> v;
+    load_pack(v, src + (chunk * 2 + 1) * static_cast<int64_t>(p.D));
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = v.v[i];
+#pragma unroll 4
+    for (int64_t k = chunk + 1; k <= last; ++k) {
+      Pack<float, VEC> u;
+      load_pack(u, src + k * 2 * static_cast<int64_t>(p.D));
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += u.v[i];
+    }
+    write_row<G, VEC>(p, cur, c, acc);
+  }
+}
+
+// Tokens a chunk: few enough that short batches fill the GPU, and at most
+// about a thousand chunks, whose partial sums are the workspace.
+int chunk_tokens(int64_t T) {
+  if (T <= 4096) return 8;
+  if (T <= 32768) return 32;
+  return static_cast<int>((T + 1023) / 1024);
+}
+
+int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
+template <class T, class G, int VEC>
+cudaError_t run_grad(GradParams p, cudaStream_t stream) {
+  const int slots = (p.D + VEC - 1) / VEC;
+  p.cols = 1;
+  while (p.cols < slots && p.cols < 256) p.cols *= 2;
+  const int rows = 256 / p.cols;
+  const dim3 grid(static_cast<unsigned>((p.chunks + rows - 1) / rows),
+                  static_cast<unsigned>((slots + p.cols - 1) / p.cols));
+  cudaError_t e = launch_dependent(grad_chunk_kernel<T, G, VEC>, grid, dim3(256), 0, stream, p);
+  if (e != cudaSuccess || p.chunks < 2) return e;
+  const int threads = std::min(256, (slots + 31) / 32 * 32);
+  const dim3 join(static_cast<unsigned>(p.chunks - 1), static_cast<unsigned>((slots + threads - 1) / threads));
+  return launch_dependent(grad_join_kernel<G, VEC>, join, dim3(threads), 0, stream, p);
+}
+
+template <class T, class G>
+cudaError_t grad_of_type(const GradParams& p, cudaStream_t stream) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  const bool wide = p.D % kVec == 0 && rows_aligned(p.dy, p.lddy, sizeof(T), 16) && rows_aligned(p.dw, p.lddw, sizeof(G), 16);
+  return wide ? run_grad<T, G, kVec>(p, stream) : run_grad<T, G, 1>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_embedding_fwd(const EmbeddingFwd& a, cudaStream_t stream) {
+  int* status = nullptr;
+  const cudaError_t e = device_status_word(&status);
+  if (e != cudaSuccess) return e;
+  const LookupParams p{a.w, a.ids, a.y, status, a.V, a.T, a.ldw, a.ldy, static_cast<int>(a.D), 0, a.scale, a.ids_i64};
+  switch (a.dtype) {
+    case FP8BQ_BF16: return lookup_to<__nv_bfloat16>(p, a.out_dtype, stream);
+    case FP8BQ_FP16: return lookup_to<__half>(p, a.out_dtype, stream);
+    default: return lookup_to<float>(p, a.out_dtype, stream);
+  }
+}
+
+int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D) {
+  if (T == 0) return 0;
+  const int64_t chunks = (T + chunk_tokens(T) - 1) / chunk_tokens(T);
+  return 2 * round256(T * static_cast<int64_t>(sizeof(Token))) + chunks * 2 * D * static_cast<int64_t>(sizeof(float));
+}
+
+cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
+  int* status = nullptr;
+  int sms = 0;
+  cudaError_t e = device_status_word(&status);
+  if (e == cudaSuccess) e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int64_t size = a.dw_dtype == FP8BQ_FP32 ? 4 : 2;
+  SortParams s{};
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const int64_t tokens_bytes = round256(a.T * static_cast<int64_t>(sizeof(Token)));
+  s.ids = a.ids;
+  s.buf[0] = reinterpret_cast<Token*>(ws);
+  s.buf[1] = reinterpret_cast<Token*>(ws + tokens_bytes);
+  s.status = status;
+  s.T = a.T;
+  s.V = a.V;
+  s.padding = a.padding;
+  s.i64 = a.ids_i64;
+  int bits = 1;
+  while ((a.V >> bits) != 0) ++bits;  // ids 0 .. V, V standing for none
+  s.passes = (bits + kDigitBits - 1) / kDigitBits;
+  s.bits = (bits + s.passes - 1) / s.passes;
+  // Few tokens: one block, without the cluster's barriers.
+  s.sorters = a.T <= 4096 ? 1 : kSortCluster;
+  const int64_t warps = static_cast<int64_t>(s.sorters) * kSortWarps;
+  s.per_warp = ((a.T + warps - 1) / warps + 31) / 32 * 32;
+  s.dw = a.accumulate ? nullptr : static_cast<uint8_t*>(a.dw);
+  s.row_bytes = a.D * size;
+  s.ld_bytes = a.lddw * size;
+  const int zeroers = a.accumulate ? 0 : (sms + kSortCluster - 1) / kSortCluster * kSortCluster;
+  constexpr size_t kSmem = sizeof(uint32_t) * kSortWarps * kBins;
+  static_assert(kSmem + sizeof(uint32_t) * (2 * kBins + kSortWarps) <= 227 * 1024, "shared memory of one block");
+  e = cudaFuncSetAttribute(sort_zero_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(s.sorters + zeroers), 1, 1);
+  cfg.blockDim = dim3(kSortThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(s.sorters);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, sort_zero_kernel, s);
+  if (e != cudaSuccess || a.T == 0) return e;
+  GradParams g{};
+  g.tokens = s.buf[0];
+  g.dy = a.dy;
+  g.dw = a.dw;
+  g.partial = reinterpret_cast<float*>(ws + 2 * tokens_bytes);
+  g.T = a.T;
+  g.V = a.V;
+  g.lddy = a.lddy;
+  g.lddw = a.lddw;
+  g.chunk = chunk_tokens(a.T);
+  g.chunks = (a.T + g.chunk - 1) / g.chunk;
+  g.D = static_cast<int>(a.D);
+  g.scale = a.scale;
+  g.accumulate = a.accumulate;
+  switch (a.dtype) {
+    case FP8BQ_BF16:
+      return a.dw_dtype == FP8BQ_FP32 ? grad_of_type<__nv_bfloat16, float>(g, stream)
+                                      : grad_of_type<__nv_bfloat16, __nv_bfloat16>(g, stream);
+    case FP8BQ_FP16:
+      return a.dw_dtype == FP8BQ_FP32 ? grad_of_type<__half, float>(g, stream) : grad_of_type<__half, __half>(g, stream);
+    default: return grad_of_type<float, float>(g, stream);
+  }
+}
+
+}  // namespace fp8bq

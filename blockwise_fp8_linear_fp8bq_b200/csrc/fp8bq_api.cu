@@ -3,9 +3,12 @@
 // memory or synchronizes, except fp8bq_check().
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "fp8bq.h"
 #include "fp8bq_testing.h"
@@ -82,6 +85,122 @@ int check_quant_args(const void* x, int64_t rows, int64_t cols, int64_t ld, cons
   if (rows < 0 || cols < 0 || ld < cols) return FP8BQ_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || (ld % 8) != 0) return FP8BQ_ERR_ALIGN;
   return FP8BQ_OK;
+}
+
+// Bytes of a row operator's element type, 0 for another dtype.
+int64_t elem_bytes(int dtype) {
+  switch (dtype) {
+    case FP8BQ_BF16:
+    case FP8BQ_FP16: return 2;
+    case FP8BQ_FP32: return 4;
+    default: return 0;
+  }
+}
+
+bool aligned_to(const void* p, int64_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
+}
+
+constexpr int64_t kMostRows = INT32_MAX - 1;
+
+// Rows and columns of a row operator.
+bool valid_rows(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows <= kMostRows && cols <= kMostRows;
+}
+
+// Token ids and the scale of an embedding call.
+int check_ids(const void* ids, int ids_i64, float scale) {
+  if ((ids_i64 != 0 && ids_i64 != 1) || !std::isfinite(scale)) return FP8BQ_ERR_INVALID_ARG;
+  return aligned_to(ids, ids_i64 ? 8 : 4) ? FP8BQ_OK : FP8BQ_ERR_ALIGN;
+}
+
+int norm_backward(const fp8bq_norm_grad* a, bool layernorm, cudaStream_t stream) {
+  if (a == nullptr) return FP8BQ_ERR_INVALID_ARG;
+  const int64_t e = elem_bytes(a->dtype);
+  if (e == 0 || (a->param_dtype != a->dtype && a->param_dtype != FP8BQ_FP32)) return FP8BQ_ERR_INVALID_ARG;
+  if ((a->flags & ~(FP8BQ_NORM_ACCUMULATE | FP8BQ_NORM_RSTD_F64)) != 0) return FP8BQ_ERR_INVALID_ARG;
+  if (!valid_rows(a->M, a->N)) return FP8BQ_ERR_SHAPE;
+  if (a->lddy < a->N || a->ldx < a->N || a->lddx < a->N || (a->dres != nullptr && a->lddres < a->N))
+    return FP8BQ_ERR_SHAPE;
+  if (a->M > 0 && a->N > 0 &&
+      (!a->dy || !a->x || !a->dx || !a->rstd || (layernorm && !a->mean)))
+    return FP8BQ_ERR_INVALID_ARG;
+  if (!aligned_to(a->dy, e) || !aligned_to(a->x, e) || !aligned_to(a->dx, e) || !aligned_to(a->dres, e) ||
+      !aligned_to(a->gamma, elem_bytes(a->param_dtype)) || !aligned_to(a->mean, 4) ||
+      !aligned_to(a->rstd, (a->flags & FP8BQ_NORM_RSTD_F64) != 0 ? 8 : 4) || !aligned_to(a->dgamma, 4) ||
+      !aligned_to(a->dbeta, 4) || !aligned16(a->workspace))
+    return FP8BQ_ERR_ALIGN;
+  fp8bq_norm_grad b = *a;
+  if (!layernorm) {
+    b.mean = nullptr;
+    b.dbeta = nullptr;
+  }
+  const bool sums = b.dgamma != nullptr || b.dbeta != nullptr;
+  if (b.N == 0 || (b.M == 0 && !sums)) return FP8BQ_OK;
+  int st = device_ok();
+  if (st != FP8BQ_OK) return st;
+  if (sums && b.M > 0) {
+    int sms = 0;
+    const cudaError_t err = fp8bq::device_sm_count(&sms);
+    if (err != cudaSuccess) return cuda_status(err);
+    if (!b.workspace || b.workspace_bytes < fp8bq::norm_bwd_workspace_bytes(b.M, b.N, sms))
+      return FP8BQ_ERR_INVALID_ARG;
+  }
+  return cuda_status(fp8bq::launch_norm_bwd(b, layernorm, stream));
+}
+
+// Whether a tensor that clipping writes overlaps another listed one (its own
+// input, at the same address, apart).
+int check_overlaps(const fp8bq_grad* grads, int count) {
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * static_cast<size_t>(count) + 1]);
+  if (!spans) return FP8BQ_ERR_UNSUPPORTED;
+  size_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    const fp8bq_grad& g = grads[i];
+    if (g.n == 0) continue;
+    const auto add = [&](const void* p, int dtype, bool written) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+      spans[n++] = Span{b, b + static_cast<uintptr_t>(g.n * elem_bytes(dtype)), written};
+    };
+    add(g.out, g.out_dtype, true);
+    if (g.g != g.out) add(g.g, g.dtype, false);
+  }
+  std::sort(spans.get(), spans.get() + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, written = 0;  // where the spans so far end
+  for (size_t i = 0; i < n; ++i) {
+    if (spans[i].begin < (spans[i].written ? any : written)) return FP8BQ_ERR_INVALID_ARG;
+    any = std::max(any, spans[i].end);
+    if (spans[i].written) written = std::max(written, spans[i].end);
+  }
+  return FP8BQ_OK;
+}
+
+int grad_list(const fp8bq_grad* grads, int count, double max_norm, bool clip, float* norm, void* workspace,
+              int64_t workspace_bytes, cudaStream_t stream) {
+  if (count < 0) return FP8BQ_ERR_SHAPE;
+  if ((grads == nullptr && count > 0) || norm == nullptr || !(max_norm >= 0.0)) return FP8BQ_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const fp8bq_grad& g = grads[i];
+    const int64_t e = elem_bytes(g.dtype), o = clip ? elem_bytes(g.out_dtype) : 1;
+    if (e == 0 || o == 0) return FP8BQ_ERR_INVALID_ARG;
+    if (g.n < 0 || g.n > (int64_t{1} << 48)) return FP8BQ_ERR_SHAPE;
+    if (g.n > 0 && (!g.g || (clip && !g.out))) return FP8BQ_ERR_INVALID_ARG;
+    if (clip && g.n > 0 && g.g == g.out && g.dtype != g.out_dtype) return FP8BQ_ERR_INVALID_ARG;
+    if (!aligned_to(g.g, e) || (clip && !aligned_to(g.out, o))) return FP8BQ_ERR_ALIGN;
+  }
+  if (!aligned_to(norm, 4) || !aligned16(workspace)) return FP8BQ_ERR_ALIGN;
+  int st = clip ? check_overlaps(grads, count) : FP8BQ_OK;
+  if (st != FP8BQ_OK) return st;
+  if ((st = device_ok()) != FP8BQ_OK) return st;
+  int sms = 0;
+  const cudaError_t err = fp8bq::device_sm_count(&sms);
+  if (err != cudaSuccess) return cuda_status(err);
+  if (!workspace || workspace_bytes < fp8bq::grad_clip_workspace_bytes(count, sms)) return FP8BQ_ERR_INVALID_ARG;
+  return cuda_status(fp8bq::launch_grad_clip(grads, count, max_norm, clip, norm, workspace, stream));
 }
 
 // Operand checks shared by A and B; fills the internal form.
@@ -305,6 +424,96 @@ int fp8bq_rmsnorm_quantize_exact(const void* x, int64_t M, int64_t K, int64_t ld
                                                        fmt, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int fp8bq_embedding_forward(const void* w, int64_t V, int64_t D, int64_t ldw, const void* ids, int ids_i64, int64_t T,
+                            float scale, void* y, int64_t ldy, int dtype, int out_dtype, fp8bq_stream_t stream) {
+  const int64_t e = elem_bytes(dtype), o = elem_bytes(out_dtype);
+  if (e == 0 || o == 0) return FP8BQ_ERR_INVALID_ARG;
+  if (!valid_rows(V, D) || T < 0 || T > kMostRows || ldw < D || ldy < D) return FP8BQ_ERR_SHAPE;
+  int st = check_ids(ids, ids_i64, scale);
+  if (st != FP8BQ_OK) return st;
+  if (!aligned_to(w, e) || !aligned_to(y, o)) return FP8BQ_ERR_ALIGN;
+  if (T == 0 || D == 0) return FP8BQ_OK;
+  if (!ids || !y || (!w && V > 0)) return FP8BQ_ERR_INVALID_ARG;
+  if ((st = device_ok()) != FP8BQ_OK) return st;
+  const fp8bq::EmbeddingFwd a{w, ids, y, V, D, ldw, T, ldy, scale, dtype, out_dtype, ids_i64 != 0};
+  return cuda_status(fp8bq::launch_embedding_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_embedding_backward(const void* dy, int64_t T, int64_t D, int64_t lddy, const void* ids, int ids_i64, int64_t V,
+                             float scale, int64_t padding_id, void* dw, int64_t lddw, int dtype, int dw_dtype,
+                             uint32_t flags, void* workspace, int64_t workspace_bytes, fp8bq_stream_t stream) {
+  const int64_t e = elem_bytes(dtype);
+  if (e == 0 || (dw_dtype != dtype && dw_dtype != FP8BQ_FP32)) return FP8BQ_ERR_INVALID_ARG;
+  if ((flags & ~static_cast<uint32_t>(FP8BQ_EMBEDDING_ACCUMULATE)) != 0) return FP8BQ_ERR_INVALID_ARG;
+  if (!valid_rows(V, D) || T < 0 || T > kMostRows || lddy < D || lddw < D) return FP8BQ_ERR_SHAPE;
+  int st = check_ids(ids, ids_i64, scale);
+  if (st != FP8BQ_OK) return st;
+  if (!aligned_to(dy, e) || !aligned_to(dw, elem_bytes(dw_dtype)) || !aligned16(workspace)) return FP8BQ_ERR_ALIGN;
+  const bool accumulate = (flags & FP8BQ_EMBEDDING_ACCUMULATE) != 0;
+  if (D == 0 || (T == 0 && (accumulate || V == 0))) return FP8BQ_OK;
+  if ((!dw && V > 0) || (T > 0 && (!dy || !ids))) return FP8BQ_ERR_INVALID_ARG;
+  if (T > 0 && (!workspace || workspace_bytes < fp8bq::embedding_bwd_workspace_bytes(T, D)))
+    return FP8BQ_ERR_INVALID_ARG;
+  if ((st = device_ok()) != FP8BQ_OK) return st;
+  const fp8bq::EmbeddingBwd a{dy,   ids,  dw,         workspace, T, D, lddy, V, lddw, padding_id, scale,
+                              dtype, dw_dtype, ids_i64 != 0, accumulate};
+  return cuda_status(fp8bq::launch_embedding_bwd(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D) {
+  return valid_rows(T, D) ? fp8bq::embedding_bwd_workspace_bytes(T, D) : -1;
+}
+
+int fp8bq_layernorm_forward(const void* x, int64_t M, int64_t N, int64_t ldx, const void* gamma, const void* beta,
+                            float eps, void* y, int64_t ldy, float* mean, float* rstd, int dtype, int param_dtype,
+                            fp8bq_stream_t stream) {
+  const int64_t e = elem_bytes(dtype);
+  if (e == 0 || (param_dtype != dtype && param_dtype != FP8BQ_FP32)) return FP8BQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return FP8BQ_ERR_INVALID_ARG;
+  if (!valid_rows(M, N) || ldx < N || ldy < N) return FP8BQ_ERR_SHAPE;
+  if (M > 0 && N > 0 && (!x || !y)) return FP8BQ_ERR_INVALID_ARG;
+  const int64_t pe = elem_bytes(param_dtype);
+  if (!aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(gamma, pe) || !aligned_to(beta, pe) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return FP8BQ_ERR_ALIGN;
+  if (M == 0 || N == 0) return FP8BQ_OK;
+  const int st = device_ok();
+  if (st != FP8BQ_OK) return st;
+  const fp8bq::NormFwd a{x, gamma, beta, y, mean, rstd, M, N, ldx, ldy, eps, dtype, param_dtype};
+  return cuda_status(fp8bq::launch_layernorm_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_layernorm_backward(const fp8bq_norm_grad* args, fp8bq_stream_t stream) {
+  return norm_backward(args, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fp8bq_rmsnorm_backward(const fp8bq_norm_grad* args, fp8bq_stream_t stream) {
+  return norm_backward(args, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t fp8bq_norm_workspace_bytes(int64_t M, int64_t N) {
+  int sms = 0;
+  if (!valid_rows(M, N) || device_ok() != FP8BQ_OK || fp8bq::device_sm_count(&sms) != cudaSuccess) return -1;
+  return fp8bq::norm_bwd_workspace_bytes(M, N, sms);
+}
+
+int fp8bq_grad_norm(const fp8bq_grad* grads, int count, float* norm, void* workspace, int64_t workspace_bytes,
+                    fp8bq_stream_t stream) {
+  return grad_list(grads, count, 0.0, false, norm, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fp8bq_grad_clip(const fp8bq_grad* grads, int count, double max_norm, float* norm, void* workspace,
+                    int64_t workspace_bytes, fp8bq_stream_t stream) {
+  return grad_list(grads, count, max_norm, true, norm, workspace, workspace_bytes,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t fp8bq_grad_workspace_bytes(int count) {
+  int sms = 0;
+  if (count < 0 || device_ok() != FP8BQ_OK || fp8bq::device_sm_count(&sms) != cudaSuccess) return -1;
+  return fp8bq::grad_clip_workspace_bytes(count, sms);
+}
+
 int fp8bq_quantize_weight(const void* w, int64_t N, int64_t K, int64_t ldw, void* q, void* scales,
                           int fmt, fp8bq_stream_t stream) {
   int st = check_quant_args(w, N, K, ldw, q, scales, fmt);
@@ -399,6 +608,7 @@ int fp8bq_check(fp8bq_stream_t stream) {
   int status = 0;
   cudaError_t e = fp8bq::read_and_clear_device_status(reinterpret_cast<cudaStream_t>(stream), &status);
   if (e != cudaSuccess) return cuda_status(e);
+  if (status == fp8bq::kStatusIndex) return FP8BQ_ERR_INDEX;
   return status != 0 ? FP8BQ_ERR_TIMEOUT : FP8BQ_OK;
 }
 
@@ -420,6 +630,7 @@ const char* fp8bq_status_string(int status) {
     case FP8BQ_ERR_UNSUPPORTED: return "unsupported device or operand combination";
     case FP8BQ_ERR_CUDA: return "CUDA error";
     case FP8BQ_ERR_TIMEOUT: return "device wait timed out";
+    case FP8BQ_ERR_INDEX: return "token id outside the embedding table";
     default: return "unknown status";
   }
 }

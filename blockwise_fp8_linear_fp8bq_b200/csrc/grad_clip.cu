@@ -1,0 +1,242 @@
+// grad_clip.cu -- the global norm of many gradients, and their clipping.
+//
+//   norm = sqrt(sum over all tensors and values of g^2)
+//   out  = g * min(1, max_norm / (norm + 1e-6))
+//
+// Bound by HBM: the values are read once for the norm and once more to be
+// scaled.  Sums are taken in a fixed order (no floating-point atomics), in
+// FP32 over eight values and in float64 beyond, so that the norm of billions
+// of values, of tiny or of huge ones is right to FP32's rounding.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "elem.cuh"
+#include "internal.h"
+
+namespace fp8bq {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kPack = 8;                         // values a thread takes at once
+constexpr int kChunk = kThreads * kPack * 4;     // values of one tensor a block takes at once
+constexpr int kTensors = 128;                    // tensors a launch takes (its parameters hold their table)
+
+struct Table {
+  const void* g[kTensors];
+  void* out[kTensors];
+  int64_t n[kTensors];
+  int64_t first[kTensors];  // the tensor's first chunk among the launch's
+  int8_t in_dtype[kTensors], out_dtype[kTensors];
+  int64_t chunks;
+  int count;
+};
+
+// The tensor that chunk k belongs to.
+__device__ __forceinline__ int tensor_of(const Table& t, int64_t k) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= k)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Eight squares in FP32 where neither the sum nor what matters of it leaves
+// the normal range, else in float64.
+template <class T>
+__device__ __forceinline__ double sum_squares(const Pack<T, kPack>& v) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPack; ++i) s = fmaf(v.f(i), v.f(i), s);
+  if (s > 0x1p-80f && s < 0x1p120f) return static_cast<double>(s);
+  double d = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPack; ++i) {
+    const double x = v.f(i);
+    if (x != 0.0) d = fma(x, x, d);
+  }
+  return d;
+}
+
+template <class T>
+__device__ __forceinline__ double chunk_squares(const void* src, int64_t begin, int64_t n) {
+  const T* g = static_cast<const T*>(src) + begin;
+  double s = 0.0;
+  if (n == kChunk && reinterpret_cast<uintptr_t>(g) % 16 == 0) {
+    Pack<T, kPack> v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_pack(v[j], g + (j * kThreads + threadIdx.x) * kPack);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += sum_squares(v[j]);
+  } else {
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kThreads * kPack) {
+      Pack<T, kPack> v;
+#pragma unroll
+      for (int j = 0; j < kPack; ++j) v.v[j] = i0 + j * kThreads < n ? g[i0 + j * kThreads] : from_float<T>(0.0f);
+      s += sum_squares(v);
+    }
+  }
+  return s;
+}
+
+__device__ __forceinline__ double block_sum(double s, double* red) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant__ Table t, double* partial) {
+  __shared__ double red[kThreads / 32];
+  double s = 0.0;
+  for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const int i = tensor_of(t, k);
+    const int64_t begin = (k - t.first[i]) * kChunk, n = min(t.n[i] - begin, static_cast<int64_t>(kChunk));
+    switch (t.in_dtype[i]) {
+      case FP8BQ_BF16: s += chunk_squares<__nv_bfloat16>(t.g[i], begin, n); break;
+      case FP8BQ_FP16: s += chunk_squares<__half>(t.g[i], begin, n); break;
+      default: s += chunk_squares<float>(t.g[i], begin, n);
+    }
+  }
+  s = block_sum(s, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// The norm from the blocks' sums: every block that calls it gets the same.
+__device__ __forceinline__ double norm_of(const double* partial, int64_t parts, double* red) {
+  double s = 0.0;
+  for (int64_t k = threadIdx.x; k < parts; k += kThreads) s += partial[k];
+  return sqrt(block_sum(s, red));
+}
+
+__global__ void __launch_bounds__(kThreads) norm_kernel(const double* partial, int64_t parts, float* norm) {
+  __shared__ double red[kThreads / 32];
+  cudaGridDependencySynchronize();
+  const double r = norm_of(partial, parts, red);
+  if (threadIdx.x == 0) *norm = static_cast<float>(r);
+}
+
+template <class T, class O>
+__device__ __forceinline__ void scale_chunk(const void* src, void* dst, int64_t begin, int64_t n, float f) {
+  const T* g = static_cast<const T*>(src) + begin;
+  O* out = static_cast<O*>(dst) + begin;
+  if (n == kChunk && (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) % 16 == 0) {
+    Pack<T, kPack> v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_pack<true>(v[j], g + (j * kThreads + threadIdx.x) * kPack);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      Pack<O, kPack> o;
+#pragma unroll
+      for (int i = 0; i < kPack; ++i) o.v[i] = from_float<O>(v[j].f(i) * f);
+      store_pack<true>(out + (j * kThreads + threadIdx.x) * kPack, o);
+    }
+  } else {
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) out[i] = from_float<O>(to_float(g[i]) * f);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void scale_to(const Table& t, int i, int64_t begin, int64_t n, float f) {
+  switch (t.out_dtype[i]) {
+    case FP8BQ_BF16: scale_chunk<T, __nv_bfloat16>(t.g[i], t.out[i], begin, n, f); break;
+    case FP8BQ_FP16: scale_chunk<T, __half>(t.g[i], t.out[i], begin, n, f); break;
+    default: scale_chunk<T, float>(t.g[i], t.out[i], begin, n, f);
+  }
+}
+
+// Chunks in the reverse of the norm's order: those read last may still be in
+// L2.  Tensors scaled in place by a factor of 1 are left alone.
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table t, const double* partial,
+                                                         int64_t parts, double max_norm, float* norm) {
+  __shared__ double red[kThreads / 32];
+  cudaGridDependencySynchronize();
+  const double r = norm_of(partial, parts, red);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(r);
+  const double q = max_norm / (r + 1e-6);
+  const float f = static_cast<float>(q >= 1.0 ? 1.0 : q);  // NaN stays NaN
+  for (int64_t k = t.chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
+    const int i = tensor_of(t, k);
+    if (f == 1.0f && t.g[i] == t.out[i]) continue;
+    const int64_t begin = (k - t.first[i]) * kChunk, n = min(t.n[i] - begin, static_cast<int64_t>(kChunk));
+    switch (t.in_dtype[i]) {
+      case FP8BQ_BF16: scale_to<__nv_bfloat16>(t, i, begin, n, f); break;
+      case FP8BQ_FP16: scale_to<__half>(t, i, begin, n, f); break;
+      default: scale_to<float>(t, i, begin, n, f);
+    }
+  }
+}
+
+// The table of tensors [at, ...) of the list that one launch takes, empty
+// tensors left out; returns where the next launch starts.
+int fill_table(const fp8bq_grad* grads, int count, int at, Table* t) {
+  t->count = 0;
+  t->chunks = 0;
+  for (; at < count && t->count < kTensors; ++at) {
+    const fp8bq_grad& g = grads[at];
+    if (g.n == 0) continue;
+    const int i = t->count++;
+    t->g[i] = g.g;
+    t->out[i] = g.out;
+    t->n[i] = g.n;
+    t->first[i] = t->chunks;
+    t->in_dtype[i] = static_cast<int8_t>(g.dtype);
+    t->out_dtype[i] = static_cast<int8_t>(g.out_dtype);
+    t->chunks += (g.n + kChunk - 1) / kChunk;
+  }
+  return at;
+}
+
+// Blocks of a launch: two for each SM, or one for each chunk.
+int64_t blocks_of(int64_t chunks, int sms) { return std::min<int64_t>(chunks, 2 * static_cast<int64_t>(sms)); }
+
+}  // namespace
+
+int64_t grad_clip_workspace_bytes(int count, int sms) {
+  const int64_t launches = std::max(1, (count + kTensors - 1) / kTensors);
+  return launches * 2 * sms * static_cast<int64_t>(sizeof(double));
+}
+
+cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm, bool clip, float* norm,
+                             void* workspace, cudaStream_t stream) {
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  double* partial = static_cast<double*>(workspace);
+  int64_t parts = 0;
+  Table t;
+  for (int at = 0; at < count;) {
+    at = fill_table(grads, count, at, &t);
+    if (t.chunks == 0) break;
+    const int64_t blocks = blocks_of(t.chunks, sms);
+    square_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(t, partial + parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    parts += blocks;
+  }
+  if (!clip || parts == 0)
+    return launch_dependent(norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(partial), parts,
+                            norm);
+  bool first = true;
+  for (int at = 0; at < count;) {
+    at = fill_table(grads, count, at, &t);
+    if (t.chunks == 0) break;
+    e = launch_dependent(scale_kernel, dim3(static_cast<unsigned>(blocks_of(t.chunks, sms))), dim3(kThreads), 0, stream, t,
+                         static_cast<const double*>(partial), parts, max_norm, first ? norm : nullptr);
+    if (e != cudaSuccess) return e;
+    first = false;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace fp8bq

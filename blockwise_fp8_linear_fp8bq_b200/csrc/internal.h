@@ -58,6 +58,70 @@ cudaError_t launch_rmsnorm_quant_exact(const void* x, int64_t M, int64_t K, int6
                                        double eps, double* rstd64, void* h, void* q, void* s_rows, void* qt,
                                        void* s_cols, int fmt, cudaStream_t stream);
 
+// What a kernel records in the device status word for a token id outside its
+// table (the bounded waits record the small codes of their places).
+constexpr int kStatusIndex = 1000;
+
+// Validated calls of the row operators, in the library's internal form.
+struct NormFwd {
+  const void* x;
+  const void* gamma;  // or NULL
+  const void* beta;   // or NULL
+  void* y;
+  float* mean;  // or NULL
+  float* rstd;  // or NULL
+  int64_t M, N, ldx, ldy;
+  float eps;
+  int dtype, param_dtype;
+};
+struct EmbeddingFwd {
+  const void* w;
+  const void* ids;
+  void* y;
+  int64_t V, D, ldw, T, ldy;
+  float scale;
+  int dtype, out_dtype;
+  bool ids_i64;
+};
+struct EmbeddingBwd {
+  const void* dy;
+  const void* ids;
+  void* dw;
+  void* workspace;
+  int64_t T, D, lddy, V, lddw, padding;
+  float scale;
+  int dtype, dw_dtype;
+  bool ids_i64, accumulate;
+};
+cudaError_t launch_layernorm_fwd(const NormFwd& a, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream_t stream);
+int64_t norm_bwd_workspace_bytes(int64_t M, int64_t N, int sms);
+cudaError_t launch_embedding_fwd(const EmbeddingFwd& a, cudaStream_t stream);
+cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream);
+int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D);
+// The norm of the listed gradients, and with `clip` their scaled copies.
+cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm, bool clip, float* norm,
+                             void* workspace, cudaStream_t stream);
+int64_t grad_clip_workspace_bytes(int count, int sms);
+
+// Launches a kernel that may be set up while the kernel before it on the
+// stream still runs; it must call cudaGridDependencySynchronize() before it
+// touches memory.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Driver entry point of cuTensorMapEncodeTiled (nullptr if unavailable).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // Multiprocessor count of the current device (cached).

@@ -62,6 +62,7 @@ typedef struct CUstream_st* fp8bq_stream_t;
                                    /* this library does not build                   */
 #define FP8BQ_ERR_CUDA (-5)        /* a CUDA call failed; see fp8bq_last_cuda_error */
 #define FP8BQ_ERR_TIMEOUT (-6)     /* a bounded wait inside a kernel expired        */
+#define FP8BQ_ERR_INDEX (-7)       /* a token id outside its embedding table        */
 
 typedef enum { FP8BQ_SCALE_FP32 = 0, FP8BQ_SCALE_UE8M0 = 1 } fp8bq_scale_fmt;
 typedef enum {
@@ -69,7 +70,9 @@ typedef enum {
   FP8BQ_GRAN_BLOCK_128x128 = 1,
   FP8BQ_GRAN_ROW_1x32 = 2 /* MX blocks: 32 consecutive contraction values, UE8M0 only */
 } fp8bq_gran;
-typedef enum { FP8BQ_E4M3 = 0, FP8BQ_BF16 = 1 } fp8bq_dtype;
+/* FP16 and FP32 are types of the row operators only (embedding, norms,
+ * gradient clipping); a GEMM operand is E4M3 or BF16. */
+typedef enum { FP8BQ_E4M3 = 0, FP8BQ_BF16 = 1, FP8BQ_FP16 = 2, FP8BQ_FP32 = 3 } fp8bq_dtype;
 
 /* fp8bq_gemm flags */
 #define FP8BQ_GEMM_ACCUMULATE_F32 1u /* D is FP32 and D += A B^T */
@@ -239,6 +242,172 @@ int fp8bq_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, con
 int fp8bq_rmsnorm_quantize_exact(const void* x, int64_t M, int64_t K, int64_t ldx, const void* gamma, double eps,
                                  double* rstd, void* h, void* q, void* scales, void* qt, void* scales_t, int fmt,
                                  fp8bq_stream_t stream);
+
+/*
+ * Row operators of a training step around the linears: embedding, LayerNorm,
+ * RMSNorm's backward pass, gradient clipping.  The pages keep what is not a
+ * linear layer's matmul, and all training state, in BF16 or FP32
+ * ("清华开源 Puro-2B", section "精度"), and name the model they belong to
+ * (the digest's "方法": Qwen3-1.7B-like, untied embedding and LM head); they
+ * describe no such call.  Shared by the calls below:
+ *   - a dtype is FP8BQ_BF16, FP8BQ_FP16 or FP8BQ_FP32; all arithmetic is FP32
+ *     or wider and every output value is rounded once, to nearest even;
+ *   - rows of any length and leading dimension, at any address a multiple of
+ *     the element size; 16-byte aligned rows whose length is a multiple of 16
+ *     bytes are moved 16 bytes at a time, others one element at a time;
+ *   - columns past the row length (up to the leading dimension) are neither
+ *     read nor written;
+ *   - sums run in an order fixed by the sizes: equal inputs on equal GPUs
+ *     give equal bits;
+ *   - a workspace is device memory, 16-byte aligned, of any content; calls
+ *     that may run at the same time need one each;
+ *   - ERR_ALIGN for a pointer not aligned to its element, ERR_SHAPE for a
+ *     negative size, a leading dimension below the row length, or more than
+ *     2^31 - 2 rows or columns; ERR_INVALID_ARG for a NULL pointer (unless
+ *     the call has nothing to read or write there) or another dtype.
+ */
+
+/*
+ * Embedding lookup with scaling: y[t, :] = scale * W[ids[t], :].
+ *   w        [V, D] of dtype, leading dimension ldw.
+ *   ids      [T], int32 (ids_i64 = 0) or int64 (ids_i64 = 1).
+ *   scale    finite (sqrt(D) in models that scale their embeddings, else 1).
+ *   y        [T, D] of out_dtype, leading dimension ldy.
+ * An id outside [0, V) reads nothing, gives a row of zeros and is reported
+ * as ERR_INDEX by the next fp8bq_check().
+ * Errors: as above; ERR_INVALID_ARG for ids_i64 not 0 or 1 or a scale that is
+ * not finite.  T == 0 or D == 0 is a no-op.
+ */
+int fp8bq_embedding_forward(const void* w, int64_t V, int64_t D, int64_t ldw, const void* ids, int ids_i64, int64_t T,
+                            float scale, void* y, int64_t ldy, int dtype, int out_dtype, fp8bq_stream_t stream);
+
+/*
+ * The table's gradient: dW[v, :] = scale * sum over t, ids[t] = v, of
+ * dY[t, :], in ascending t within chunks of tokens; rows no id names are
+ * zeros.
+ *   dy          [T, D] of dtype, leading dimension lddy.
+ *   ids, ids_i64, scale  as in the lookup.
+ *   padding_id  tokens with this id add nothing (a negative value: none).
+ *   dw          [V, D] of dw_dtype (dtype or FP8BQ_FP32), leading dimension
+ *               lddw.
+ *   flags       0, or FP8BQ_EMBEDDING_ACCUMULATE: dW += the sum (FP32 master
+ *               gradients), each value rounded once; rows no id names are
+ *               then neither read nor written.
+ *   workspace   fp8bq_embedding_workspace_bytes(T, D) bytes.
+ * An id outside [0, V) adds nothing and is reported as by the lookup.
+ * Errors: as the lookup; ERR_INVALID_ARG for other flag bits, a dw_dtype
+ * other than the two, or a workspace too small.
+ */
+#define FP8BQ_EMBEDDING_ACCUMULATE 1u
+int fp8bq_embedding_backward(const void* dy, int64_t T, int64_t D, int64_t lddy, const void* ids, int ids_i64, int64_t V,
+                             float scale, int64_t padding_id, void* dw, int64_t lddw, int dtype, int dw_dtype,
+                             uint32_t flags, void* workspace, int64_t workspace_bytes, fp8bq_stream_t stream);
+/* Workspace bytes of fp8bq_embedding_backward; -1 on bad arguments. */
+int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D);
+
+/*
+ * LayerNorm: y = (x - mean) * rstd * gamma + beta, mean and rstd = 1 /
+ * sqrt(avg((x - mean)^2) + eps) over each row's N values.
+ *   x, y         [M, N] of dtype, leading dimensions ldx, ldy; y may be x.
+ *   gamma, beta  [N] of param_dtype (dtype or FP8BQ_FP32), or NULL (1 and 0).
+ *   eps          finite, >= 0.
+ *   mean, rstd   FP32 [M], written (what the backward pass needs), or NULL.
+ * Squares of x - mean must not overflow FP32.
+ * Errors: as above; ERR_INVALID_ARG for a bad eps.  M == 0 or N == 0 is a
+ * no-op.
+ */
+int fp8bq_layernorm_forward(const void* x, int64_t M, int64_t N, int64_t ldx, const void* gamma, const void* beta,
+                            float eps, void* y, int64_t ldy, float* mean, float* rstd, int dtype, int param_dtype,
+                            fp8bq_stream_t stream);
+
+/*
+ * The backward passes of LayerNorm and of RMSNorm (h = x * rstd * gamma, as
+ * fp8bq_rmsnorm_quantize computes it).  With xh = (x - mean) * rstd (RMSNorm:
+ * x * rstd) and g = dy * gamma, averages over the row:
+ *   LayerNorm  dx = rstd * (g - avg(g) - xh * avg(g * xh)) + dres
+ *   RMSNorm    dx = rstd * (g - xh * avg(g * xh)) + dres
+ *   dgamma = sum over rows of dy * xh, dbeta = sum over rows of dy.
+ *   dy, x, dx   [M, N] of dtype, each with its leading dimension; dx may be
+ *               dy, x or dres with the same leading dimension.
+ *   dres        [M, N] of dtype, added to dx (the gradient that reaches x
+ *               past the norm, along the residual stream), or NULL.
+ *   gamma       [N] of param_dtype (dtype or FP8BQ_FP32), or NULL (1).
+ *   mean        FP32 [M] (LayerNorm; RMSNorm ignores it).
+ *   rstd        FP32 [M], or float64 [M] with FP8BQ_NORM_RSTD_F64 (what
+ *               fp8bq_rmsnorm_quantize_exact gives).
+ *   dgamma, dbeta  FP32 [N], written, or added to with
+ *               FP8BQ_NORM_ACCUMULATE; either may be NULL (RMSNorm ignores
+ *               dbeta).
+ *   flags       0 or the two above.
+ *   workspace   fp8bq_norm_workspace_bytes(M, N) bytes; may be NULL when
+ *               neither dgamma nor dbeta is wanted.
+ * With M == 0, dgamma and dbeta are zeros (or left as they are); N == 0 is a
+ * no-op.
+ * Errors: as above; ERR_INVALID_ARG for other flag bits or a workspace too
+ * small.
+ */
+#define FP8BQ_NORM_ACCUMULATE 1u
+#define FP8BQ_NORM_RSTD_F64 2u
+typedef struct fp8bq_norm_grad {
+  const void* dy;
+  const void* x;
+  const void* dres;
+  void* dx;
+  int64_t M, N;
+  int64_t lddy, ldx, lddres, lddx;
+  const void* gamma;
+  const float* mean;
+  const void* rstd;
+  float* dgamma;
+  float* dbeta;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t dtype, param_dtype;
+  uint32_t flags;
+  int32_t reserved; /* set to 0 */
+} fp8bq_norm_grad;
+int fp8bq_layernorm_backward(const fp8bq_norm_grad* args, fp8bq_stream_t stream);
+int fp8bq_rmsnorm_backward(const fp8bq_norm_grad* args, fp8bq_stream_t stream);
+/* Workspace bytes of the norms' backward passes on the current device; -1 on
+ * bad arguments or without a usable device. */
+int64_t fp8bq_norm_workspace_bytes(int64_t M, int64_t N);
+
+/*
+ * The global norm of a list of gradients and their clipping:
+ *   norm = sqrt(sum over all tensors and values of g^2),
+ *   out  = g * min(1, max_norm / (norm + 1e-6)).
+ *   grads   HOST array of `count` tensors: g, n contiguous values of dtype;
+ *           out, n values of out_dtype (any of the three), either g itself
+ *           (then of the same dtype; a factor of 1 leaves it untouched) or
+ *           memory that overlaps no listed tensor.  fp8bq_grad_norm ignores out and
+ *           out_dtype.  The array may be freed when the call returns.  n == 0
+ *           is allowed, and then g and out may be NULL.
+ *   max_norm  >= 0 (infinite: only the norm's NaN changes anything).
+ *   norm    FP32 [1], written: the norm before clipping.  The sum is taken
+ *           beyond FP32's range, so that it is finite where the norm is.  A
+ *           NaN among the values makes the norm and every out NaN; an
+ *           infinity makes the norm infinite and the factor 0 (its own out
+ *           is then NaN).  An empty list has norm 0.
+ *   workspace  fp8bq_grad_workspace_bytes(count) bytes.
+ * Errors: as above; ERR_INVALID_ARG for a max_norm below 0 or NaN, an out
+ * that is g with another dtype or that overlaps another tensor of the list
+ * (a tensor listed twice among them), or a workspace too small; ERR_SHAPE
+ * for count < 0 or n outside 0 .. 2^48.
+ */
+typedef struct fp8bq_grad {
+  const void* g;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+  int32_t out_dtype;
+} fp8bq_grad;
+int fp8bq_grad_norm(const fp8bq_grad* grads, int count, float* norm, void* workspace, int64_t workspace_bytes,
+                    fp8bq_stream_t stream);
+int fp8bq_grad_clip(const fp8bq_grad* grads, int count, double max_norm, float* norm, void* workspace,
+                    int64_t workspace_bytes, fp8bq_stream_t stream);
+/* Workspace bytes of the two on the current device; -1 on a negative count or
+ * without a usable device. */
+int64_t fp8bq_grad_workspace_bytes(int count);
 
 /*
  * MX-block quantization (1x32 groups, UE8M0 scales): the other reading of
@@ -422,7 +591,8 @@ int64_t fp8bq_scales_bytes(int gran, int fmt, int64_t rows, int64_t contraction)
 /*
  * Synchronizes `stream`, then reports the first device-side failure since the
  * last check: FP8BQ_ERR_TIMEOUT if a GEMM kernel's bounded wait expired (the
- * kernel then stopped early and its output is undefined), FP8BQ_ERR_CUDA if
+ * kernel then stopped early and its output is undefined), FP8BQ_ERR_INDEX if
+ * an embedding call met a token id outside its table, FP8BQ_ERR_CUDA if
  * the stream reported an error.  Clears the recorded state.
  */
 int fp8bq_check(fp8bq_stream_t stream);
