@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -53,21 +54,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
     extra = ["-Xptxas", "-v"] if ptxas_info else []
-    for src in _sources():
+
+    def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0 or (verbose and r.stderr):
-            sys.stderr.write(r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
-        if ptxas_info:
-            sys.stderr.write(r.stderr)
-        objs.append(obj)
+        return src, obj, subprocess.run(cmd, capture_output=True, text=True)
+
+    objs = []
+    with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        for src, obj, r in pool.map(compile_one, _sources()):
+            if r.returncode != 0 or ((verbose or ptxas_info) and r.stderr):
+                sys.stderr.write(r.stderr)
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+            objs.append(obj)
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     if verbose:

@@ -28,12 +28,33 @@ __device__ __forceinline__ __half from_float<__half>(float v) {
   return __float2half_rn(v);
 }
 
+// Two values, in one instruction where they share a register.
+__device__ __forceinline__ float2 to_float2(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 to_float2(const __nv_bfloat16* v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(v));
+}
+__device__ __forceinline__ float2 to_float2(const __half* v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(v));
+}
+__device__ __forceinline__ void from_float2(float* d, float2 v) {
+  d[0] = v.x;
+  d[1] = v.y;
+}
+__device__ __forceinline__ void from_float2(__nv_bfloat16* d, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(d) = __float22bfloat162_rn(v);
+}
+__device__ __forceinline__ void from_float2(__half* d, float2 v) {
+  *reinterpret_cast<__half2*>(d) = __float22half2_rn(v);
+}
+
 // VEC consecutive elements, moved in accesses of up to 16 bytes; the address
 // is aligned to the smaller of 16 bytes and the pack's size.
 template <class T, int VEC>
 struct alignas(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
   T v[VEC];
   __device__ __forceinline__ float f(int i) const { return to_float(v[i]); }
+  __device__ __forceinline__ float2 f2(int i) const { return to_float2(v + 2 * i); }  // values 2 i, 2 i + 1
+  __device__ __forceinline__ void set2(int i, float2 w) { from_float2(v + 2 * i, w); }
 };
 
 // STREAM: read once, so evicted first from the caches.
