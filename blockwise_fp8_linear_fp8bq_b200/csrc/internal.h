@@ -104,9 +104,10 @@ cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm
                              void* workspace, cudaStream_t stream);
 int64_t grad_clip_workspace_bytes(int count, int sms);
 
-// Launches a kernel that may be set up while the kernel before it on the
-// stream still runs; it must call cudaGridDependencySynchronize() before it
-// touches memory.
+// Launches a kernel that may start while the kernel before it on the stream
+// still runs (once that one's blocks have all ended or allowed it); it must
+// call cudaGridDependencySynchronize() before it touches what that one reads
+// or writes.
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
