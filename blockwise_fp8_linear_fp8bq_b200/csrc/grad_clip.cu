@@ -18,10 +18,13 @@
 namespace fp8bq {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kPack = 8;                         // values a thread takes at once
-constexpr int kChunk = kThreads * kPack * 4;     // values of one tensor a block takes at once
-constexpr int kTensors = 128;                    // tensors a launch takes (its parameters hold their table)
+constexpr int kThreads = 256;
+constexpr int kPack = 8;                      // values a thread takes at once
+constexpr int kUnit = kThreads * kPack;       // values a block takes at once
+constexpr int kUnits = 2;                     // units of a chunk
+constexpr int kChunk = kUnits * kUnit;        // values of one tensor a block takes before it looks for more
+constexpr int kNormBlocks = 8;                // blocks for each SM that take the norm
+constexpr int kTensors = 128;                 // tensors a launch takes (its parameters hold their table)
 
 struct Table {
   const void* g[kTensors];
@@ -63,23 +66,30 @@ __device__ __forceinline__ double sum_squares(const Pack<T, kPack>& v) {
   return d;
 }
 
+// A chunk of n values from g on: whole packs where g is 16-byte aligned (two
+// in flight a thread), then value by value.
 template <class T>
-__device__ __forceinline__ double chunk_squares(const void* src, int64_t begin, int64_t n) {
-  const T* g = static_cast<const T*>(src) + begin;
+__device__ __forceinline__ double chunk_squares(const T* g, int n) {
   double s = 0.0;
-  if (n == kChunk && reinterpret_cast<uintptr_t>(g) % 16 == 0) {
-    Pack<T, kPack> v[4];
+  const int packs = reinterpret_cast<uintptr_t>(g) % 16 == 0 ? n / kPack : 0;
+  if (packs == kUnits * kThreads) {
+    Pack<T, kPack> v[kUnits];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_pack(v[j], g + (j * kThreads + threadIdx.x) * kPack);
+    for (int j = 0; j < kUnits; ++j) load_pack(v[j], g + (j * kThreads + threadIdx.x) * kPack);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s += sum_squares(v[j]);
-  } else {
-    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kThreads * kPack) {
-      Pack<T, kPack> v;
+    for (int j = 0; j < kUnits; ++j) s += sum_squares(v[j]);
+    return s;
+  }
+  for (int i = threadIdx.x; i < packs; i += kThreads) {
+    Pack<T, kPack> v;
+    load_pack(v, g + i * kPack);
+    s += sum_squares(v);
+  }
+  for (int i0 = packs * kPack + threadIdx.x; i0 < n; i0 += kThreads * kPack) {
+    Pack<T, kPack> v;
 #pragma unroll
-      for (int j = 0; j < kPack; ++j) v.v[j] = i0 + j * kThreads < n ? g[i0 + j * kThreads] : from_float<T>(0.0f);
-      s += sum_squares(v);
-    }
+    for (int j = 0; j < kPack; ++j) v.v[j] = i0 + j * kThreads < n ? g[i0 + j * kThreads] : from_float<T>(0.0f);
+    s += sum_squares(v);
   }
   return s;
 }
@@ -100,11 +110,12 @@ __global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant_
   double s = 0.0;
   for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const int i = tensor_of(t, k);
-    const int64_t begin = (k - t.first[i]) * kChunk, n = min(t.n[i] - begin, static_cast<int64_t>(kChunk));
+    const int64_t begin = (k - t.first[i]) * kChunk;
+    const int n = static_cast<int>(min(t.n[i] - begin, static_cast<int64_t>(kChunk)));
     switch (t.in_dtype[i]) {
-      case FP8BQ_BF16: s += chunk_squares<__nv_bfloat16>(t.g[i], begin, n); break;
-      case FP8BQ_FP16: s += chunk_squares<__half>(t.g[i], begin, n); break;
-      default: s += chunk_squares<float>(t.g[i], begin, n);
+      case FP8BQ_BF16: s += chunk_squares(static_cast<const __nv_bfloat16*>(t.g[i]) + begin, n); break;
+      case FP8BQ_FP16: s += chunk_squares(static_cast<const __half*>(t.g[i]) + begin, n); break;
+      default: s += chunk_squares(static_cast<const float*>(t.g[i]) + begin, n);
     }
   }
   s = block_sum(s, red);
@@ -118,62 +129,84 @@ __device__ __forceinline__ double norm_of(const double* partial, int64_t parts, 
   return sqrt(block_sum(s, red));
 }
 
-__global__ void __launch_bounds__(kThreads) norm_kernel(const double* partial, int64_t parts, float* norm) {
+// The factor; NaN where the norm is.
+__device__ __forceinline__ float factor_of(double norm, double max_norm) {
+  const double q = max_norm / (norm + 1e-6);
+  return static_cast<float>(q >= 1.0 ? 1.0 : q);
+}
+
+// The norm, and the factor for a scaling kernel of many blocks.
+__global__ void __launch_bounds__(kThreads) norm_kernel(const double* partial, int64_t parts, double max_norm, float* norm,
+                                                        float* factor) {
   __shared__ double red[kThreads / 32];
   cudaGridDependencySynchronize();
   const double r = norm_of(partial, parts, red);
-  if (threadIdx.x == 0) *norm = static_cast<float>(r);
+  if (threadIdx.x != 0) return;
+  *norm = static_cast<float>(r);
+  if (factor != nullptr) *factor = factor_of(r, max_norm);
 }
 
 template <class T, class O>
-__device__ __forceinline__ void scale_chunk(const void* src, void* dst, int64_t begin, int64_t n, float f) {
-  const T* g = static_cast<const T*>(src) + begin;
-  O* out = static_cast<O*>(dst) + begin;
-  if (n == kChunk && (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) % 16 == 0) {
-    Pack<T, kPack> v[4];
+__device__ __forceinline__ void scale_chunk(const T* g, O* out, int n, float f) {
+  const int packs = (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) % 16 == 0 ? n / kPack : 0;
+  const auto put = [&](const Pack<T, kPack>& v, int i) {
+    Pack<O, kPack> o;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_pack<true>(v[j], g + (j * kThreads + threadIdx.x) * kPack);
+    for (int j = 0; j < kPack; ++j) o.v[j] = from_float<O>(v.f(j) * f);
+    store_pack<true>(out + i * kPack, o);
+  };
+  if (packs == kUnits * kThreads) {
+    Pack<T, kPack> v[kUnits];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Pack<O, kPack> o;
+    for (int j = 0; j < kUnits; ++j) load_pack<true>(v[j], g + (j * kThreads + threadIdx.x) * kPack);
 #pragma unroll
-      for (int i = 0; i < kPack; ++i) o.v[i] = from_float<O>(v[j].f(i) * f);
-      store_pack<true>(out + (j * kThreads + threadIdx.x) * kPack, o);
-    }
-  } else {
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) out[i] = from_float<O>(to_float(g[i]) * f);
+    for (int j = 0; j < kUnits; ++j) put(v[j], j * kThreads + threadIdx.x);
+    return;
   }
+  for (int i = threadIdx.x; i < packs; i += kThreads) {
+    Pack<T, kPack> v;
+    load_pack<true>(v, g + i * kPack);
+    put(v, i);
+  }
+#pragma unroll 4
+  for (int i = packs * kPack + threadIdx.x; i < n; i += kThreads) out[i] = from_float<O>(to_float(g[i]) * f);
 }
 
 template <class T>
-__device__ __forceinline__ void scale_to(const Table& t, int i, int64_t begin, int64_t n, float f) {
+__device__ __forceinline__ void scale_to(const Table& t, int i, int64_t begin, int n, float f) {
+  const T* g = static_cast<const T*>(t.g[i]) + begin;
   switch (t.out_dtype[i]) {
-    case FP8BQ_BF16: scale_chunk<T, __nv_bfloat16>(t.g[i], t.out[i], begin, n, f); break;
-    case FP8BQ_FP16: scale_chunk<T, __half>(t.g[i], t.out[i], begin, n, f); break;
-    default: scale_chunk<T, float>(t.g[i], t.out[i], begin, n, f);
+    case FP8BQ_BF16: scale_chunk(g, static_cast<__nv_bfloat16*>(t.out[i]) + begin, n, f); break;
+    case FP8BQ_FP16: scale_chunk(g, static_cast<__half*>(t.out[i]) + begin, n, f); break;
+    default: scale_chunk(g, static_cast<float*>(t.out[i]) + begin, n, f);
   }
 }
 
-// Chunks in the reverse of the norm's order: those read last may still be in
-// L2.  Tensors scaled in place by a factor of 1 are left alone.
+// One chunk a block, in the reverse of the norm's order: those read last may
+// still be in L2.  A short list's blocks take the factor from the norm's
+// partial sums themselves (factor NULL).  Tensors scaled in place by a factor
+// of 1 are left alone.
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table t, const double* partial,
-                                                         int64_t parts, double max_norm, float* norm) {
+                                                         int64_t parts, double max_norm, float* norm, const float* factor) {
   __shared__ double red[kThreads / 32];
   cudaGridDependencySynchronize();
-  const double r = norm_of(partial, parts, red);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(r);
-  const double q = max_norm / (r + 1e-6);
-  const float f = static_cast<float>(q >= 1.0 ? 1.0 : q);  // NaN stays NaN
-  for (int64_t k = t.chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
-    const int i = tensor_of(t, k);
-    if (f == 1.0f && t.g[i] == t.out[i]) continue;
-    const int64_t begin = (k - t.first[i]) * kChunk, n = min(t.n[i] - begin, static_cast<int64_t>(kChunk));
-    switch (t.in_dtype[i]) {
-      case FP8BQ_BF16: scale_to<__nv_bfloat16>(t, i, begin, n, f); break;
-      case FP8BQ_FP16: scale_to<__half>(t, i, begin, n, f); break;
-      default: scale_to<float>(t, i, begin, n, f);
-    }
+  float f;
+  if (factor != nullptr) {
+    f = *factor;
+  } else {
+    const double r = norm_of(partial, parts, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(r);
+    f = factor_of(r, max_norm);
+  }
+  const int64_t k = t.chunks - 1 - blockIdx.x;
+  const int i = tensor_of(t, k);
+  if (f == 1.0f && t.g[i] == t.out[i]) return;
+  const int64_t begin = (k - t.first[i]) * kChunk;
+  const int n = static_cast<int>(min(t.n[i] - begin, static_cast<int64_t>(kChunk)));
+  switch (t.in_dtype[i]) {
+    case FP8BQ_BF16: scale_to<__nv_bfloat16>(t, i, begin, n, f); break;
+    case FP8BQ_FP16: scale_to<__half>(t, i, begin, n, f); break;
+    default: scale_to<float>(t, i, begin, n, f);
   }
 }
 
@@ -197,14 +230,14 @@ int fill_table(const fp8bq_grad* grads, int count, int at, Table* t) {
   return at;
 }
 
-// Blocks of a launch: two for each SM, or one for each chunk.
-int64_t blocks_of(int64_t chunks, int sms) { return std::min<int64_t>(chunks, 2 * static_cast<int64_t>(sms)); }
+// Blocks of the norm's launch.
+int64_t blocks_of(int64_t chunks, int sms) { return std::min<int64_t>(chunks, kNormBlocks * static_cast<int64_t>(sms)); }
 
 }  // namespace
 
 int64_t grad_clip_workspace_bytes(int count, int sms) {
   const int64_t launches = std::max(1, (count + kTensors - 1) / kTensors);
-  return launches * 2 * sms * static_cast<int64_t>(sizeof(double));
+  return 16 + launches * kNormBlocks * sms * static_cast<int64_t>(sizeof(double));
 }
 
 cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm, bool clip, float* norm,
@@ -212,8 +245,9 @@ cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  double* partial = static_cast<double*>(workspace);
-  int64_t parts = 0;
+  float* factor = static_cast<float*>(workspace);
+  double* partial = static_cast<double*>(workspace) + 2;
+  int64_t parts = 0, chunks = 0;
   Table t;
   for (int at = 0; at < count;) {
     at = fill_table(grads, count, at, &t);
@@ -223,16 +257,22 @@ cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     parts += blocks;
+    chunks += t.chunks;
   }
-  if (!clip || parts == 0)
-    return launch_dependent(norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(partial), parts,
-                            norm);
-  bool first = true;
+  const bool many = chunks > 4 * static_cast<int64_t>(sms);
+  if (!clip || parts == 0 || many) {
+    e = launch_dependent(norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(partial), parts, max_norm,
+                         norm, clip ? factor : nullptr);
+    if (e != cudaSuccess || !clip) return e;
+  }
+  bool first = !many;
   for (int at = 0; at < count;) {
     at = fill_table(grads, count, at, &t);
     if (t.chunks == 0) break;
-    e = launch_dependent(scale_kernel, dim3(static_cast<unsigned>(blocks_of(t.chunks, sms))), dim3(kThreads), 0, stream, t,
-                         static_cast<const double*>(partial), parts, max_norm, first ? norm : nullptr);
+    if (t.chunks > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_dependent(scale_kernel, dim3(static_cast<unsigned>(t.chunks)), dim3(kThreads), 0, stream, t,
+                         static_cast<const double*>(partial), parts, max_norm, first ? norm : nullptr,
+                         many ? static_cast<const float*>(factor) : nullptr);
     if (e != cudaSuccess) return e;
     first = false;
   }

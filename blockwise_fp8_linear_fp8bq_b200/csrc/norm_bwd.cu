@@ -1,0 +1,432 @@
+// norm_bwd.cu -- the backward passes of LayerNorm and RMSNorm.
+//
+//   xh = (x - mean) * rstd (RMSNorm: mean = 0), g = dy * gamma
+//   dx = rstd * (g - avg(g) - xh * avg(g * xh)) [+ dres]  (RMSNorm: without avg(g))
+//   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+//
+// FP32 arithmetic, dx rounded once.  Bound by HBM: x, dy and dres are read
+// once, through a ring of rows in shared memory.  A thread keeps its columns
+// for the whole launch, their dgamma and dbeta in registers; the blocks' sums
+// go to the workspace and are added in a fixed order by a second kernel.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "row_ring.cuh"
+
+namespace fp8bq {
+namespace {
+
+struct BwdParams {
+  const void* dy;
+  const void* x;
+  const void* dres;  // or NULL
+  void* dx;
+  const void* gamma;  // or NULL
+  const float* mean;
+  const void* rstd;
+  float* partial;  // [blocks][LN ? 2 : 1][N] sums of dgamma, dbeta, or NULL
+  int64_t M, N, lddy, ldx, lddres, lddx;
+  float inv_n;
+  bool p32, rstd64;
+  int tpr;  // threads a row, a multiple of 32
+};
+
+__device__ __forceinline__ float load_rstd(const BwdParams& p, int64_t row) {
+  return p.rstd64 ? static_cast<float>(static_cast<const double*>(p.rstd)[row]) : static_cast<const float*>(p.rstd)[row];
+}
+
+// tpr threads a row, COLS columns each, R rows a thread between two barriers;
+// x and dy are read from shared memory twice, before and after the row's
+// sums.  RES: dres is given.
+template <class T, int COLS, int R, bool LN, bool RES, bool ALIGNED, bool FULL>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ BwdParams p,
+                                                       const __grid_constant__ RingParams rp) {
+  constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 8, G = COLS / W;
+  constexpr int K = LN ? 2 * R : R;               // sums a thread takes part in
+  constexpr bool kGammaRegs = COLS <= 16;         // else read again for each row
+  using Cols = Group<T, W, ALIGNED, FULL>;
+  using Sums = Group<float, W, ALIGNED, FULL>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][16][K];
+  __shared__ __align__(8) uint64_t bars[kMostStages];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tpr = p.tpr, groups = blockDim.x / tpr;
+  const int group = tid / tpr, t = tid - group * tpr;
+  const int warps = tpr >> 5, warp0 = group * warps;
+  const int n = rp.n;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * rp.rows;
+  int64_t block_row = static_cast<int64_t>(blockIdx.x) * rp.rows;
+  RowRing<T, RES ? 3 : 2, ALIGNED> ring(rp, smem, bars, &abort_flag, block_row, row_step);
+  ring.init(tid == 0);
+  if (warp == 0) ring.start();
+
+  float2 gam[kGammaRegs ? G : 1][W / 2];
+  float2 dg[G][W / 2], db[G][W / 2];
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    if constexpr (kGammaRegs) Cols::load_param(gam[j], p.gamma, p.p32, 1.0f, t, tpr, j, n);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) dg[j][i] = db[j][i] = make_float2(0.0f, 0.0f);
+  }
+  // The rows' statistics, fetched one row block ahead: lane r holds row r's
+  // rstd, lane R + r its mean; zeros for rows past the last.
+  const float* stat = LN && lane >= R ? p.mean : static_cast<const float*>(p.rstd);
+  const int stat_row = LN && lane >= R ? lane - R : lane;
+  const bool stat_lane = lane < K && !(p.rstd64 && lane < R);
+  float next = 0.0f;
+  double next64 = 0.0;
+  auto statistics = [&](int64_t row) {
+    next = 0.0f;
+    if (stat_lane && row + stat_row < rp.M) next = stat[row + stat_row];
+    if (p.rstd64) {
+      next64 = 0.0;
+      if (lane < R && row + lane < rp.M) next64 = static_cast<const double*>(p.rstd)[row + lane];
+    }
+  };
+  statistics(block_row + group * R);
+
+  int buf = 0;
+  for (bool begun = false; block_row < rp.M; block_row += row_step, buf ^= 1, begun = true) {
+    const int64_t row0 = block_row + group * R;
+    float2 mean[R];  // negated
+    float rstd[R];
+    if (p.rstd64 && lane < R) next = static_cast<float>(next64);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = __shfl_sync(0xffffffffu, next, r);
+      const float a = LN ? -__shfl_sync(0xffffffffu, next, R + r) : 0.0f;
+      mean[r] = make_float2(a, a);
+    }
+    statistics(row0 + row_step);
+    const int live = static_cast<int>(min(static_cast<int64_t>(R), rp.M - row0));  // rows of this group, or less than 1
+    ring.wait();
+    if (live < R) {  // rows past the last add nothing: each thread clears the values it reads
+      const float2 zeros[W / 2] = {};
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+          if (r >= live) {
+            Cols::store(ring.row(0, block_row, group * R + r), zeros, t, tpr, j, n);
+            Cols::store(ring.row(1, block_row, group * R + r), zeros, t, tpr, j, n);
+          }
+    }
+    float v[K];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const T* sx = ring.row(0, block_row, group * R + r);
+      const T* sy = ring.row(1, block_row, group * R + r);
+      float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+      const float2 rs = make_float2(rstd[r], rstd[r]);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        float2 x[W / 2], y[W / 2], gj[W / 2];
+        Cols::load(x, sx, t, tpr, j, n);
+        Cols::load(y, sy, t, tpr, j, n);
+        if constexpr (!kGammaRegs) Cols::load_param(gj, p.gamma, p.p32, 1.0f, t, tpr, j, n);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const float2 g = __fmul2_rn(y[i], kGammaRegs ? gam[kGammaRegs ? j : 0][i] : gj[i]);
+          const float2 xh = __fmul2_rn(LN ? __fadd2_rn(x[i], mean[r]) : x[i], rs);
+          if (LN) s1 = __fadd2_rn(s1, g);
+          s2 = __ffma2_rn(g, xh, s2);
+          dg[j][i] = __ffma2_rn(y[i], xh, dg[j][i]);
+          if (LN) db[j][i] = __fadd2_rn(db[j][i], y[i]);
+        }
+      }
+      v[r] = s2.x + s2.y;
+      if constexpr (LN) v[R + r] = s1.x + s1.y;
+    }
+    int index;
+    const float part = warp_sums<K>(v, lane, index);
+    if ((lane & (32 / K - 1)) == 0) red[buf][warp][index] = part;
+    __syncthreads();  // the last use of red[buf] and of the previous stage is over
+    if (warp == 0 && begun) ring.fetch();
+    // lane w * K + k adds value k of every (32 / K)-th warp from w on
+    float sum = 0.0f;
+    for (int w = lane / K; w < warps; w += 32 / K) sum += red[buf][warp0 + w][lane % K];
+#pragma unroll
+    for (int o = K; o < 32; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum *= -p.inv_n;
+    // dx = rstd * g + (-rstd * c1) + (x - mean) * (-rstd^2 * c2)
+    T* dx = static_cast<T*>(p.dx) + row0 * p.lddx;
+#pragma unroll
+    for (int r = 0; r < R; ++r, dx += p.lddx) {
+      const float k2 = __shfl_sync(0xffffffffu, sum, r) * rstd[r] * rstd[r];
+      const float k1 = LN ? __shfl_sync(0xffffffffu, sum, (R + r) % 32) * rstd[r] : 0.0f;
+      if (r >= live) break;
+      const float2 c1 = make_float2(k1, k1), c2 = make_float2(k2, k2), rs = make_float2(rstd[r], rstd[r]);
+      const T* sx = ring.row(0, block_row, group * R + r);
+      const T* sy = ring.row(1, block_row, group * R + r);
+      const T* sr = ring.row(RES ? 2 : 0, block_row, group * R + r);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        float2 x[W / 2], y[W / 2], z[W / 2], gj[W / 2];
+        Cols::load(x, sx, t, tpr, j, n);
+        Cols::load(y, sy, t, tpr, j, n);
+        if (RES) Cols::load(z, sr, t, tpr, j, n);
+        if constexpr (!kGammaRegs) Cols::load_param(gj, p.gamma, p.p32, 1.0f, t, tpr, j, n);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const float2 g = __fmul2_rn(y[i], kGammaRegs ? gam[kGammaRegs ? j : 0][i] : gj[i]);
+          float2 d = LN ? __ffma2_rn(__fadd2_rn(x[i], mean[r]), c2, c1) : __fmul2_rn(x[i], c2);
+          d = __ffma2_rn(g, rs, d);
+          x[i] = RES ? __fadd2_rn(d, z[i]) : d;
+        }
+        Cols::store(dx, x, t, tpr, j, n);
+      }
+    }
+    ring.next();
+  }
+  if (ring.finish(tid == 0) || p.partial == nullptr) return;
+  // the block's groups in order, through the ring's memory (no copy is in
+  // flight any more), then one row of sums
+  float* join = reinterpret_cast<float*>(smem);  // [LN ? 2 : 1][N]
+  for (int k = 1; k < groups; ++k) {
+    __syncthreads();
+    if (group == k) {
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        Sums::store(join, dg[j], t, tpr, j, n);
+        if (LN) Sums::store(join + n, db[j], t, tpr, j, n);
+      }
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        float2 a[W / 2], b[W / 2];
+        Sums::load(a, join, t, tpr, j, n);
+        if (LN) Sums::load(b, join + n, t, tpr, j, n);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          dg[j][i] = __fadd2_rn(dg[j][i], a[i]);
+          if (LN) db[j][i] = __fadd2_rn(db[j][i], b[i]);
+        }
+      }
+    }
+  }
+  if (group == 0) {
+    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * (LN ? 2 : 1) * n;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      Sums::store(out, dg[j], t, tpr, j, n);
+      if (LN) Sums::store(out + n, db[j], t, tpr, j, n);
+    }
+  }
+}
+
+// Rows too long for a block: the sums over rows column by
+// column, and dx row by row (read twice).
+template <class T, bool LN>
+__global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const BwdParams p) {
+  __shared__ float2 red[32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+  const T* res = static_cast<const T*>(p.dres) + row * p.lddres;
+  const float mean = LN ? p.mean[row] : 0.0f, rstd = load_rstd(p, row);
+  const auto gamma = [&](int64_t c) {
+    return p.gamma == nullptr ? 1.0f
+           : p.p32            ? static_cast<const float*>(p.gamma)[c]
+                              : to_float(static_cast<const T*>(p.gamma)[c]);
+  };
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int64_t c = threadIdx.x; c < p.N; c += blockDim.x) {
+    const float g = to_float(dy[c]) * gamma(c);
+    s.x += g;
+    s.y = fmaf(g, (to_float(x[c]) - mean) * rstd, s.y);
+  }
+  s = block_sum2(s, red);
+  const float c1 = LN ? s.x * p.inv_n : 0.0f, c2 = s.y * p.inv_n;
+  T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+  for (int64_t c = threadIdx.x; c < p.N; c += blockDim.x) {
+    float g = fmaf(to_float(dy[c]), gamma(c), -c1);
+    g = fmaf(-((to_float(x[c]) - mean) * rstd), c2, g) * rstd;
+    if (p.dres != nullptr) g += to_float(res[c]);
+    dx[c] = from_float<T>(g);
+  }
+}
+
+template <class T, bool LN>
+__global__ void __launch_bounds__(256) norm_cols_kernel(const BwdParams p) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= p.N) return;
+  float dg = 0.0f, db = 0.0f;
+#pragma unroll 4
+  for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y) {
+    const float d = to_float(static_cast<const T*>(p.dy)[row * p.lddy + c]);
+    const float xv = to_float(static_cast<const T*>(p.x)[row * p.ldx + c]);
+    dg = fmaf(d, (xv - (LN ? p.mean[row] : 0.0f)) * load_rstd(p, row), dg);
+    db += d;
+  }
+  float* out = p.partial + static_cast<int64_t>(blockIdx.y) * (LN ? 2 : 1) * p.N;
+  out[c] = dg;
+  if (LN) out[p.N + c] = db;
+}
+
+// dgamma and dbeta from the blocks' partial sums, in a fixed order: a block
+// takes 32 columns, its 16 warps every 16th partial each.
+__global__ void __launch_bounds__(512) norm_param_grad_kernel(const float* __restrict__ partial, int64_t parts,
+                                                              int64_t width, int64_t N, float* dgamma, float* dbeta,
+                                                              bool accumulate) {
+  __shared__ float red[16][33];
+  cudaGridDependencySynchronize();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float s = 0.0f;
+  if (c < width) {
+#pragma unroll 4
+    for (int64_t k = warp; k < parts; k += 16) s += partial[k * width + c];
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= width) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += red[w][lane];
+  float* out = c < N ? dgamma : dbeta;
+  if (out == nullptr) return;
+  out += c < N ? c : c - N;
+  *out = accumulate ? *out + s : s;
+}
+
+// As many rows between two barriers as leave the ring two stages (measured at
+// [16384, 2048] BF16 with a residual, LayerNorm, 8 columns a thread: 75 us with
+// one row, 57 with two, 51 with four).
+RowPlan plan_bwd(int64_t M, int64_t N, int64_t size, int tensors, bool aligned, bool packed, int sms) {
+  const int least = aligned ? static_cast<int>(16 / size) : 8;
+  const RowChoice choices[] = {{256, least, 4}, {256, 8, 4}, {256, 16, 2}, {512, 16, 2}, {512, 32, 1}};
+  if (aligned && (N * size) % 16 != 0) return RowPlan{};
+  return plan_rows(choices, 5, M, N, size, tensors, aligned, packed, sms, [](int threads, int) { return threads > 256 ? 1 : 2; });
+}
+
+// Rows too long for a block: the blocks that share each column's sum.
+int64_t long_blocks(int64_t M, int64_t N, int sms) {
+  return std::min<int64_t>(M, std::max<int64_t>(1, 4 * sms / ((N + 255) / 256)));
+}
+
+template <class T, int COLS, int R, bool LN, bool RES, bool ALIGNED, bool FULL>
+cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
+  p.tpr = b.tpr;
+  const auto kern = norm_bwd_kernel<T, COLS, R, LN, RES, ALIGNED, FULL>;
+  const int64_t smem = std::max<int64_t>(static_cast<int64_t>(b.ring.stage_bytes) * b.ring.stages,
+                                         b.groups > 1 ? p.N * (LN ? 8 : 4) : 0);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(b.blocks), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+  return cudaGetLastError();
+}
+
+template <class T, int COLS, int R, bool LN, bool ALIGNED>
+cudaError_t run_rows(const BwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  if constexpr (ALIGNED)
+    if (p.N == static_cast<int64_t>(b.tpr) * COLS)
+      return p.dres != nullptr ? run_as<T, COLS, R, LN, true, true, true>(p, b, stream)
+                               : run_as<T, COLS, R, LN, false, true, true>(p, b, stream);
+  return p.dres != nullptr ? run_as<T, COLS, R, LN, true, ALIGNED, false>(p, b, stream)
+                           : run_as<T, COLS, R, LN, false, ALIGNED, false>(p, b, stream);
+}
+
+template <class T, int COLS, bool LN, bool ALIGNED>
+cudaError_t run(const BwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  if constexpr (COLS <= 8)
+    if (b.rows == 4) return run_rows<T, COLS, 4, LN, ALIGNED>(p, b, stream);
+  if constexpr (COLS <= 16)
+    if (b.rows == 2) return run_rows<T, COLS, 2, LN, ALIGNED>(p, b, stream);
+  return run_rows<T, COLS, 1, LN, ALIGNED>(p, b, stream);
+}
+
+template <class T, bool LN, bool ALIGNED>
+cudaError_t run_plan(const BwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  if constexpr (ALIGNED && sizeof(T) == 4)
+    if (b.cols == 4) return run<T, 4, LN, ALIGNED>(p, b, stream);
+  switch (b.cols) {
+    case 8: return run<T, 8, LN, ALIGNED>(p, b, stream);
+    case 16: return run<T, 16, LN, ALIGNED>(p, b, stream);
+    default: return run<T, 32, LN, ALIGNED>(p, b, stream);
+  }
+}
+
+template <class T, bool LN>
+cudaError_t bwd_of_type(const BwdParams& p, RowPlan& b, bool aligned, int64_t blocks, cudaStream_t stream) {
+  if (b.cols == 0) {
+    if (p.partial != nullptr) {  // before dx, which may be written over dy or x
+      const dim3 grid(static_cast<unsigned>((p.N + 255) / 256), static_cast<unsigned>(blocks));
+      norm_cols_kernel<T, LN><<<grid, 256, 0, stream>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    norm_bwd_long_kernel<T, LN><<<static_cast<unsigned>(p.M), 1024, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  return aligned ? run_plan<T, LN, true>(p, b, stream) : run_plan<T, LN, false>(p, b, stream);
+}
+
+}  // namespace
+
+int64_t norm_bwd_workspace_bytes(int64_t M, int64_t N, int sms) {
+  if (M == 0 || N == 0) return 0;
+  int64_t most = long_blocks(M, N, sms);
+  for (int64_t size : {2, 4})
+    for (int tensors : {2, 3})
+      for (int how = 0; how < 4; ++how)
+        most = std::max(most, plan_bwd(M, N, size, tensors, (how & 1) != 0, (how & 2) != 0, sms).blocks);
+  return most * 2 * N * static_cast<int64_t>(sizeof(float));
+}
+
+cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream_t stream) {
+  int sms = 0;
+  int* status = nullptr;
+  cudaError_t e = device_sm_count(&sms);
+  if (e == cudaSuccess) e = device_status_word(&status);
+  if (e != cudaSuccess) return e;
+  const bool sums = a.dgamma != nullptr || a.dbeta != nullptr;
+  int64_t blocks = 0;
+  if (a.M > 0) {
+    const int64_t size = a.dtype == FP8BQ_FP32 ? 4 : 2;
+    const bool res = a.dres != nullptr;
+    const bool aligned = (a.N * size) % 16 == 0 && rows_aligned(a.x, a.ldx, size, 16) &&
+                         rows_aligned(a.dy, a.lddy, size, 16) && rows_aligned(a.dx, a.lddx, size, 16) &&
+                         (!res || rows_aligned(a.dres, a.lddres, size, 16)) && rows_aligned(a.gamma, 0, 1, 16);
+    const bool packed = a.ldx == a.N && a.lddy == a.N && (!res || a.lddres == a.N);
+    RowPlan b = plan_bwd(a.M, a.N, size, res ? 3 : 2, aligned, packed, sms);
+    blocks = b.cols != 0 ? b.blocks : long_blocks(a.M, a.N, sms);
+    b.ring.src[0] = a.x;
+    b.ring.src[1] = a.dy;
+    b.ring.src[2] = a.dres;
+    b.ring.ld[0] = a.ldx;
+    b.ring.ld[1] = a.lddy;
+    b.ring.ld[2] = a.lddres;
+    b.ring.status = status;
+    const BwdParams p{a.dy, a.x, a.dres, a.dx, a.gamma, a.mean, a.rstd, sums ? static_cast<float*>(a.workspace) : nullptr,
+                      a.M, a.N, a.lddy, a.ldx, a.lddres, a.lddx, 1.0f / static_cast<float>(a.N),
+                      a.param_dtype == FP8BQ_FP32, (a.flags & FP8BQ_NORM_RSTD_F64) != 0, 0};
+    switch (a.dtype) {
+      case FP8BQ_BF16:
+        e = layernorm ? bwd_of_type<__nv_bfloat16, true>(p, b, aligned, blocks, stream)
+                      : bwd_of_type<__nv_bfloat16, false>(p, b, aligned, blocks, stream);
+        break;
+      case FP8BQ_FP16:
+        e = layernorm ? bwd_of_type<__half, true>(p, b, aligned, blocks, stream)
+                      : bwd_of_type<__half, false>(p, b, aligned, blocks, stream);
+        break;
+      default:
+        e = layernorm ? bwd_of_type<float, true>(p, b, aligned, blocks, stream)
+                      : bwd_of_type<float, false>(p, b, aligned, blocks, stream);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  if (!sums) return cudaSuccess;
+  const int64_t width = a.N * (layernorm ? 2 : 1);
+  return launch_dependent(norm_param_grad_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(512), 0, stream,
+                          static_cast<const float*>(a.workspace), blocks, width, a.N, a.dgamma,
+                          layernorm ? a.dbeta : nullptr, (a.flags & FP8BQ_NORM_ACCUMULATE) != 0);
+}
+
+}  // namespace fp8bq

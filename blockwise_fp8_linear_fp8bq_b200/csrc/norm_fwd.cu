@@ -1,0 +1,320 @@
+// norm_fwd.cu -- LayerNorm's forward pass (RMSNorm's is the quantizing producer
+// in quant_tiles.cu).
+//
+//   mean = avg(x), var = avg((x - mean)^2), rstd = 1 / sqrt(var + eps)
+//   y = (x - mean) * rstd * gamma + beta
+//
+// FP32 arithmetic, y rounded once.  Bound by HBM: every value is read once,
+// through a ring of rows in shared memory, and worked on in registers.  The
+// statistics take two passes over those registers: each warp sums its columns
+// and then, about its own mean, their deviations and squares; the warps'
+// results are joined about the first warp's mean, so that rows far from zero
+// lose nothing and one barrier serves the rows between it and the next.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "row_ring.cuh"
+
+namespace fp8bq {
+namespace {
+
+struct FwdParams {
+  const void* x;
+  void* y;
+  const void* gamma;
+  const void* beta;
+  float* mean;
+  float* rstd;
+  int64_t N, ldx, ldy;
+  float n, eps;
+  bool p32;  // gamma and beta are FP32 (else the rows' type)
+  int tpr;   // threads a row, a multiple of 32
+};
+
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  return __fdiv_rn(1.0f, __fsqrt_rn(fmaxf(var, 0.0f) + eps));
+}
+
+// A team of tpr threads takes a row at a time, COLS columns a thread, which
+// stay in registers from one pass to the next.  Teams share nothing but gamma
+// and beta: SHARED keeps those in shared memory, as FP32 pairs, else (the
+// longest rows, one team a block) in registers.  Few threads with many
+// columns, because the sums over a team cost as much for one column as for
+// many: at [16384, 2048] BF16, 256-thread teams of 8 columns ran at 3.1 TB/s.
+template <class T, int COLS, bool ALIGNED, bool FULL, bool SHARED>
+__global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const __grid_constant__ FwdParams p,
+                                                     const __grid_constant__ RingParams rp) {
+  constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 8, G = COLS / W;
+  using Cols = Group<T, W, ALIGNED, FULL>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[16][kMostStages];
+  __shared__ int abort_flag;
+  __shared__ float centre[2][16], sums[2][16], squares[2][16], held[16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tpr = p.tpr, team = tid / tpr, t = tid - team * tpr, teams = blockDim.x / tpr;
+  const int warps = tpr >> 5, warp0 = team * warps;
+  const int n = rp.n;
+
+  const int64_t first_row = blockIdx.x + static_cast<int64_t>(gridDim.x) * team;  // rows over the SMs first
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  float4* const params = reinterpret_cast<float4*>(smem);  // [COLS / 2][tpr]: a pair's gammas, its betas
+  uint8_t* const rings = smem + (SHARED ? COLS / 2 * tpr * static_cast<int>(sizeof(float4)) : 0);
+  RowRing<T, 1, ALIGNED> ring(rp, rings + team * rp.stages * rp.stage_bytes, bars[team], &abort_flag, first_row, step);
+  ring.init(t == 0);
+  if (warp == warp0) ring.start();
+
+  float2 gam[SHARED ? 1 : G][W / 2], bet[SHARED ? 1 : G][W / 2];
+  if constexpr (SHARED) {
+    for (int j = team; j < G; j += teams) {
+      float2 g[W / 2], b[W / 2];
+      Cols::load_param(g, p.gamma, p.p32, 1.0f, t, tpr, j, n);
+      Cols::load_param(b, p.beta, p.p32, 0.0f, t, tpr, j, n);
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) params[(j * (W / 2) + i) * tpr + t] = make_float4(g[i].x, g[i].y, b[i].x, b[i].y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      Cols::load_param(gam[j], p.gamma, p.p32, 1.0f, t, tpr, j, n);
+      Cols::load_param(bet[j], p.beta, p.p32, 0.0f, t, tpr, j, n);
+    }
+  }
+  float count = 0.0f;  // this warp's columns
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+#pragma unroll
+    for (int k = 0; k < W; ++k) count += FULL || Cols::column(t, tpr, j, k) < n ? 1.0f : 0.0f;
+  count = warp_sum(count);
+  const float inv_count = count > 0.0f ? __fdiv_rn(1.0f, count) : 0.0f;
+  if (lane == 0) held[warp] = count;
+  __syncthreads();
+
+  int buf = 0;
+  for (int64_t row = first_row; row < rp.M; row += step, buf ^= 1) {
+    ring.wait();
+    const T* x = ring.row(0, row, 0);
+    float2 v[G][W / 2];
+    float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      Cols::load(v[j], x, t, tpr, j, n);
+#pragma unroll
+      for (int i = 0; i < W / 2; i += 2) {
+        sum = __fadd2_rn(sum, v[j][i]);
+        sum2 = __fadd2_rn(sum2, v[j][i + 1]);
+      }
+    }
+    sum = __fadd2_rn(sum, sum2);
+    const float mid = warp_sum(sum.x + sum.y) * inv_count;
+    const float2 m2 = make_float2(-mid, -mid);
+    float2 sq = make_float2(0.0f, 0.0f), sq2 = sq;
+    sum = sum2 = sq;
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        float2& d = v[j][i];
+        d = __fadd2_rn(d, m2);
+        if (!FULL && Cols::column(t, tpr, j, 2 * i) >= n) d.x = 0.0f;
+        if (!FULL && Cols::column(t, tpr, j, 2 * i + 1) >= n) d.y = 0.0f;
+        float2& s = i % 2 ? sum2 : sum;
+        float2& q = i % 2 ? sq2 : sq;
+        s = __fadd2_rn(s, d);
+        q = __ffma2_rn(d, d, q);
+      }
+    sum = __fadd2_rn(sum, sum2);
+    sq = __fadd2_rn(sq, sq2);
+    float part[2] = {sum.x + sum.y, sq.x + sq.y};
+    int index;
+    const float both = warp_sums<2>(part, lane, index);
+    float s = warp_sum_of<2>(both, 0), q = warp_sum_of<2>(both, 1);
+    // the row's mean is base + avg: base a rounded mean, avg what it is off by
+    float base = mid, avg, var;
+    if (warps > 1) {
+      if (lane == 0) {
+        centre[buf][warp] = mid;
+        sums[buf][warp] = s;
+        squares[buf][warp] = q;
+      }
+      named_bar_sync(team + 1, tpr);  // the row is in the team's registers
+      if (warp == warp0) ring.fetch();
+      base = centre[buf][warp0];
+      const int w = warp0 + (lane < warps ? lane : 0);
+      const float c = lane < warps ? held[w] : 0.0f, off = centre[buf][w] - base, sw = lane < warps ? sums[buf][w] : 0.0f;
+      avg = __fdiv_rn(warp_sum(fmaf(c, off, sw)), p.n);
+      // about the mean: sum (d + a)^2 = sum d^2 + 2 a sum d + count a^2
+      const float a = off - avg;
+      var = __fdiv_rn(warp_sum(lane < warps ? fmaf(a, fmaf(c, a, 2.0f * sw), squares[buf][w]) : 0.0f), p.n);
+    } else {
+      __syncwarp();
+      ring.fetch();
+      avg = __fdiv_rn(s, p.n);
+      var = __fdiv_rn(fmaf(-avg, s, q), p.n);
+    }
+    const float rstd = rstd_of(var, p.eps);
+    if (t == 0) {
+      if (p.mean != nullptr) p.mean[row] = base + avg;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+    const float a = mid - base - avg;
+    const float2 a2 = make_float2(a, a), rs2 = make_float2(rstd, rstd);
+    T* y = static_cast<T*>(p.y) + row * p.ldy;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        float2 g, b;
+        if constexpr (SHARED) {
+          const float4 both_params = params[(j * (W / 2) + i) * tpr + t];
+          g = make_float2(both_params.x, both_params.y);
+          b = make_float2(both_params.z, both_params.w);
+        } else {
+          g = gam[j][i];
+          b = bet[j][i];
+        }
+        v[j][i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j][i], a2), rs2), g, b);
+      }
+      Cols::store(y, v[j], t, tpr, j, n);
+    }
+    ring.next();
+  }
+  ring.finish(t == 0);
+}
+
+// Rows too long for a block: read three times.
+template <class T>
+__global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const FwdParams p) {
+  __shared__ float2 red[2][32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int64_t c = threadIdx.x; c < p.N; c += blockDim.x) s.x += to_float(x[c]);
+  const float m = __fdiv_rn(block_sum2(s, red[0]).x, p.n);
+  s = make_float2(0.0f, 0.0f);
+  for (int64_t c = threadIdx.x; c < p.N; c += blockDim.x) {
+    const float d = to_float(x[c]) - m;
+    s.x += d;
+    s.y = fmaf(d, d, s.y);
+  }
+  s = block_sum2(s, red[1]);
+  const float avg = __fdiv_rn(s.x, p.n), rstd = rstd_of(__fdiv_rn(fmaf(-avg, s.x, s.y), p.n), p.eps);
+  if (threadIdx.x == 0) {
+    if (p.mean != nullptr) p.mean[row] = m + avg;
+    if (p.rstd != nullptr) p.rstd[row] = rstd;
+  }
+  T* y = static_cast<T*>(p.y) + row * p.ldy;
+  const auto param = [&](const void* v, int64_t c, float none) {
+    return v == nullptr ? none : p.p32 ? static_cast<const float*>(v)[c] : to_float(static_cast<const T*>(v)[c]);
+  };
+  for (int64_t c = threadIdx.x; c < p.N; c += blockDim.x)
+    y[c] = from_float<T>(fmaf((to_float(x[c]) - m - avg) * rstd, param(p.gamma, c, 1.0f), param(p.beta, c, 0.0f)));
+}
+
+template <class T, int COLS, bool ALIGNED, bool FULL, bool SHARED>
+cudaError_t run_as(FwdParams p, const RowPlan& b, cudaStream_t stream) {
+  p.tpr = b.tpr;
+  const auto kern = ln_fwd_kernel<T, COLS, ALIGNED, FULL, SHARED>;
+  const int smem = static_cast<int>(b.ring.stage_bytes) * b.ring.stages * b.groups + (SHARED ? b.tpr * COLS * 8 : 0);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(b.blocks), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+  return cudaGetLastError();
+}
+
+template <class T, int COLS, bool ALIGNED, bool SHARED>
+cudaError_t run(const FwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  if constexpr (ALIGNED)
+    if (p.N == static_cast<int64_t>(b.tpr) * COLS) return run_as<T, COLS, true, true, SHARED>(p, b, stream);
+  return run_as<T, COLS, ALIGNED, false, SHARED>(p, b, stream);
+}
+
+template <class T, bool ALIGNED>
+cudaError_t run_plan(const FwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  switch (b.cols) {
+    case 8: return run<T, 8, ALIGNED, true>(p, b, stream);
+    case 16: return run<T, 16, ALIGNED, true>(p, b, stream);
+    case 32: return b.tpr == 32 ? run<T, 32, ALIGNED, true>(p, b, stream) : run<T, 32, ALIGNED, false>(p, b, stream);
+    case 48: return run<T, 48, ALIGNED, true>(p, b, stream);
+    default: return run<T, 64, ALIGNED, true>(p, b, stream);
+  }
+}
+
+// Teams of one warp where 64 columns a thread hold the row, else the team and
+// columns (48 or 64) that leave the fewest idle; as many teams a block, up to
+// 16 warps, as leave each two stages.  The longest rows, whose gamma and beta
+// do not fit beside two stages, take one team of 32 columns a thread.
+RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, int sms) {
+  RowPlan b{};
+  const int64_t row = N * size, pitch = aligned ? row : (row + 30) / 16 * 16;
+  for (int cols : {8, 16, 32})
+    if (b.cols == 0 && N <= 32 * cols) {
+      b.cols = cols;
+      b.tpr = 32;
+    }
+  if (b.cols == 0) {
+    const auto threads = [&](int cols) { return static_cast<int>(((N + cols - 1) / cols + 31) / 32 * 32); };
+    b.cols = threads(48) * 48 < threads(64) * 64 ? 48 : 64;
+    b.tpr = threads(b.cols);
+  }
+  const int on_sm = b.cols <= 16 ? 2 : 1;  // blocks of 16 warps that the registers allow
+  int64_t room = kRingBytes / on_sm - kRingExtra - static_cast<int64_t>(b.tpr) * b.cols * 8;
+  b.groups = static_cast<int>(std::min<int64_t>(512 / b.tpr, room / (2 * pitch)));
+  int per_sm = on_sm;
+  if (b.groups < 1) {
+    b.cols = 32;
+    b.tpr = static_cast<int>(((N + 31) / 32 + 31) / 32 * 32);
+    b.groups = 1;
+    per_sm = 1;
+    room = kRingBytes - kRingExtra;
+    if (b.tpr > 512 || room < 2 * pitch) return RowPlan{};
+  }
+  b.rows = 1;
+  b.blocks = std::min<int64_t>(M, static_cast<int64_t>(per_sm) * sms);
+  b.ring.M = M;
+  b.ring.n = static_cast<int>(N);
+  b.ring.rows = 1;
+  b.ring.stages = static_cast<int>(std::min<int64_t>(kMostStages, room / (b.groups * pitch)));
+  b.ring.row_bytes = static_cast<uint32_t>(row);
+  b.ring.pitch = b.ring.tensor_bytes = b.ring.stage_bytes = static_cast<uint32_t>(pitch);
+  b.ring.packed = false;
+  return b;
+}
+
+template <class T>
+cudaError_t fwd_of_type(const NormFwd& a, int sms, int* status, cudaStream_t stream) {
+  const FwdParams p{a.x, a.y, a.gamma, a.beta, a.mean, a.rstd, a.N, a.ldx, a.ldy, static_cast<float>(a.N), a.eps,
+                    a.param_dtype == FP8BQ_FP32, 0};
+  const bool aligned = (a.N * sizeof(T)) % 16 == 0 && rows_aligned(a.x, a.ldx, sizeof(T), 16) &&
+                       rows_aligned(a.y, a.ldy, sizeof(T), 16) && rows_aligned(a.gamma, 0, 1, 16) &&
+                       rows_aligned(a.beta, 0, 1, 16);
+  RowPlan b = plan_fwd(a.M, a.N, sizeof(T), aligned, sms);
+  if (b.cols == 0) {
+    ln_fwd_long_kernel<T><<<static_cast<unsigned>(a.M), 1024, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  b.ring.src[0] = a.x;
+  b.ring.ld[0] = a.ldx;
+  b.ring.status = status;
+  return aligned ? run_plan<T, true>(p, b, stream) : run_plan<T, false>(p, b, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_layernorm_fwd(const NormFwd& a, cudaStream_t stream) {
+  int sms = 0;
+  int* status = nullptr;
+  cudaError_t e = device_sm_count(&sms);
+  if (e == cudaSuccess) e = device_status_word(&status);
+  if (e != cudaSuccess) return e;
+  switch (a.dtype) {
+    case FP8BQ_BF16: return fwd_of_type<__nv_bfloat16>(a, sms, status, stream);
+    case FP8BQ_FP16: return fwd_of_type<__half>(a, sms, status, stream);
+    default: return fwd_of_type<float>(a, sms, status, stream);
+  }
+}
+
+}  // namespace fp8bq

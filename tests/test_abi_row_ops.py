@@ -9,6 +9,8 @@ import torch
 
 OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, CUDA = 0, -1, -2, -3, -4, -5
 P = 1 << 20
+# With a device, an accepted call would launch on the fake pointers.
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="fake device pointers: only where there is no GPU")
 NODEV = (CUDA, UNSUPPORTED)  # every argument accepted: no device here
 BF16, FP16, FP32 = 1, 2, 3
 
@@ -127,7 +129,7 @@ def test_grad_list_arguments(L):
     assert f(G(odt=FP32)) == INVALID                           # in place with another type
     assert f(G(), most=-1.0) == INVALID and f(G(), most=float("nan")) == INVALID
     assert f(G(), norm=None) == INVALID
-    assert f(G(n=-1)) == SHAPE and f(G(n=2 ** 48 + 1)) == SHAPE and f(G(), count=-1) == SHAPE
+    assert f(G(n=-1)) == SHAPE and f(G(n=2 ** 36 + 1)) == SHAPE and f(G(), count=-1) == SHAPE
     assert f(G(g=P + 1)) == ALIGN and f(G(out=P + 1)) == ALIGN and f(G(g=P + 4096, out=P + 2, odt=FP32)) == ALIGN
     assert f(G(), norm=P + 2) == ALIGN and f(G(), ws=P + 8) == ALIGN
     # overlaps: a tensor listed twice, an output over another input, and neighbours that touch
