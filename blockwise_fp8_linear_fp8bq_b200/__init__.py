@@ -172,7 +172,7 @@ def lib():
         L.fp8bq_embedding_backward.argtypes = [vp, i64, i64, i64, vp, i32, i64, f32, i64, vp, i64, i32, i32, u32, vp, i64,
                                                vp]
         L.fp8bq_embedding_workspace_bytes.restype = i64
-        L.fp8bq_embedding_workspace_bytes.argtypes = [i64, i64]
+        L.fp8bq_embedding_workspace_bytes.argtypes = [i64, i64, i64]
         L.fp8bq_layernorm_forward.restype = i32
         L.fp8bq_layernorm_forward.argtypes = [vp, i64, i64, i64, vp, vp, f32, vp, i64, vp, vp, i32, i32, vp]
         for name in ("fp8bq_layernorm_backward", "fp8bq_rmsnorm_backward"):
@@ -541,64 +541,82 @@ def linear_wgrad(dy: torch.Tensor, x: torch.Tensor, fmt: int = SCALE_FP32) -> to
 
 _ROW_DTYPES = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 _ID_DTYPES = {torch.int32: 0, torch.int64: 1}
+_F32 = torch.float32
 
 
-def _row_dtype(t: torch.Tensor, name: str) -> int:
+def _rows(t: torch.Tensor, name: str):
+    """Checks a 2-D row-major bf16, fp16 or fp32 CUDA tensor: (dtype code, leading dimension)."""
     code = _ROW_DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bf16, fp16 or fp32")
-    return code
-
-
-def _rows(t: torch.Tensor, name: str, shape=None, dtype=None, device=None) -> int:
-    """Checks a 2-D row-major CUDA tensor and gives its leading dimension."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D row-major tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
+    ld, inner = t.stride()
+    rows, cols = shape
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D row-major tensor")
     if not t.is_cuda:
         raise ValueError("fp8bq runs on CUDA tensors only (no CPU path)")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return code, ld if rows > 1 or ld >= cols else cols
 
 
-def _vector(t: Optional[torch.Tensor], name: str, n: int, dtypes, device) -> Optional[int]:
-    """Checks an optional contiguous vector of n entries and gives its address."""
-    if t is None:
-        return None
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous vector of {n} entries ({', '.join(map(str, dtypes))}) on {device}")
+def _rows_like(t: torch.Tensor, name: str, x: torch.Tensor) -> int:
+    """The leading dimension of a tensor of x's shape, dtype and device."""
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+        raise ValueError(f"{name} must be a {x.dtype} tensor of shape {tuple(x.shape)} on {x.device}")
+    return _rows(t, name)[1]
+
+
+def _new_rows(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtypes, device: int) -> int:
+    """Checks a contiguous vector of n entries and gives its address."""
+    if t.dtype not in dtypes or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries ({', '.join(map(str, dtypes))}) on device {device}")
     return t.data_ptr()
 
 
-def _run(device: torch.device, what: str, *args) -> None:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() without its Stream object
+
+
+def _run(device: int, what: str, *args) -> None:
     """Calls the library with `device` current, on its current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _raise(getattr(lib(), what)(*args, stream), what)
+    stream = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    f = getattr(_lib or lib(), what)
+    if torch.cuda.current_device() == device:
+        status = f(*args, stream)
     else:
         with torch.cuda.device(device):
-            _raise(getattr(lib(), what)(*args, stream), what)
+            status = f(*args, stream)
+    if status != 0:
+        _raise(status, what)
 
 
-def _workspace_bytes(device: torch.device, what: str, *args) -> int:
-    if torch.cuda.current_device() == device.index:
-        n = getattr(lib(), what)(*args)
+def _workspace(device: int, like: torch.Tensor, what: str, *args):
+    """A workspace of the size that `what` gives with `device` current: (tensor or None for
+    none, its address, its bytes)."""
+    f = getattr(_lib or lib(), what)
+    if torch.cuda.current_device() == device:
+        n = f(*args)
     else:
         with torch.cuda.device(device):
-            n = getattr(lib(), what)(*args)
+            n = f(*args)
     if n < 0:
         raise RuntimeError(f"{what}: bad arguments or no usable device")
-    return n
+    if n == 0:
+        return None, None, 0
+    ws = like.new_empty(n, dtype=torch.uint8)
+    return ws, ws.data_ptr(), n
 
 
-def _ids(ids: torch.Tensor, device) -> int:
-    if ids.dtype not in _ID_DTYPES or not ids.is_contiguous() or ids.device != device:
-        raise ValueError(f"ids must be a contiguous int32 or int64 tensor on {device}")
-    return _ID_DTYPES[ids.dtype]
+def _ids(ids: torch.Tensor, device: int) -> int:
+    wide = _ID_DTYPES.get(ids.dtype)
+    if wide is None or ids.get_device() != device or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous int32 or int64 tensor on device {device}")
+    return wide
 
 
 def embedding_forward(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
@@ -606,14 +624,21 @@ def embedding_forward(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, ou
     """scale * w[ids]: w [V, D] bf16, fp16 or fp32, ids int32 or int64 of any shape ->
     [*ids.shape, D] in `dtype` (w's by default), or `out`, a row-major [ids.numel(), D].
     An id outside [0, V) gives zeros and makes the next check() raise."""
-    code, ldw = _row_dtype(w, "w"), _rows(w, "w")
+    code, ldw = _rows(w, "w")
     V, D = w.shape
-    wide, T = _ids(ids, w.device), ids.numel()
-    y = torch.empty((T, D), dtype=dtype or w.dtype, device=w.device) if out is None else out
-    ldy = _rows(y, "out", (T, D), dtype, w.device)
-    _run(w.device, "fp8bq_embedding_forward", w.data_ptr(), V, D, ldw, ids.data_ptr(), wide, T, float(scale),
-         y.data_ptr(), ldy, code, _row_dtype(y, "out"))
-    return y.view(*ids.shape, D) if out is None else y
+    device = w.get_device()
+    wide, T = _ids(ids, device), ids.numel()
+    if out is None:
+        y = w.new_empty((*ids.shape, D), dtype=dtype)
+        ycode, ldy = code if dtype is None else _ROW_DTYPES.get(dtype, 0), D
+    else:
+        y = out
+        ycode, ldy = _rows(y, "out")
+        if y.shape != (T, D) or y.get_device() != device or (dtype is not None and y.dtype != dtype):
+            raise ValueError(f"out must have shape {(T, D)}, the dtype asked for and w's device")
+    _run(device, "fp8bq_embedding_forward", w.data_ptr(), V, D, ldw, ids.data_ptr(), wide, T, scale, y.data_ptr(), ldy,
+         code, ycode)
+    return y
 
 
 EMBEDDING_ACCUMULATE = 1
@@ -630,21 +655,27 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: f
     T = ids.numel()
     D = dy.shape[-1] if dy.dim() > 0 else 0
     if dy.dim() != 2:
-        if tuple(dy.shape) != (*ids.shape, D) or not dy.is_contiguous():
+        if dy.shape != (*ids.shape, D) or not dy.is_contiguous():
             raise ValueError("dy must be [ids.numel(), D], or contiguous [*ids.shape, D]")
         dy = dy.view(T, D)
-    code, lddy = _row_dtype(dy, "dy"), _rows(dy, "dy", (T, D))
-    wide = _ids(ids, dy.device)
+    code, lddy = _rows(dy, "dy")
+    if dy.shape[0] != T:
+        raise ValueError("dy must have a row for each id")
+    device = dy.get_device()
+    wide = _ids(ids, device)
     if out is None:
         if accumulate:
             raise ValueError("accumulate=True needs the tensor to add into")
-        out = torch.empty((vocab, D), dtype=dtype, device=dy.device)
-    lddw = _rows(out, "out", (vocab, D), None, dy.device)
-    n = _workspace_bytes(dy.device, "fp8bq_embedding_workspace_bytes", T, D)
-    ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
-    _run(dy.device, "fp8bq_embedding_backward", dy.data_ptr(), T, D, lddy, ids.data_ptr(), wide, vocab, float(scale),
-         -1 if padding_id is None else padding_id, out.data_ptr(), lddw, code, _row_dtype(out, "out"),
-         EMBEDDING_ACCUMULATE if accumulate else 0, ws.data_ptr(), n)
+        out = dy.new_empty((vocab, D), dtype=dtype)
+        wcode, lddw = _ROW_DTYPES.get(dtype, 0), D
+    else:
+        wcode, lddw = _rows(out, "out")
+        if out.shape != (vocab, D) or out.get_device() != device:
+            raise ValueError(f"out must have shape {(vocab, D)} and dy's device")
+    ws, pw, n = _workspace(device, dy, "fp8bq_embedding_workspace_bytes", T, D, vocab)
+    _run(device, "fp8bq_embedding_backward", dy.data_ptr(), T, D, lddy, ids.data_ptr(), wide, vocab, scale,
+         -1 if padding_id is None else padding_id, out.data_ptr(), lddw, code, wcode,
+         EMBEDDING_ACCUMULATE if accumulate else 0, pw, n)
     return out
 
 
@@ -653,20 +684,24 @@ def layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, bet
     """x [M, N] bf16, fp16 or fp32, gamma and beta [N] (x's dtype or fp32, or None) ->
     (y, mean, rstd): y = (x - mean) * rstd * gamma + beta in x's dtype, mean and rstd
     fp32 [M].  `out` may pass (y, mean, rstd) to write into (y may be x)."""
-    code, ldx = _row_dtype(x, "x"), _rows(x, "x")
+    code, ldx = _rows(x, "x")
     M, N = x.shape
-    dev = x.device
-    pdt = next((p.dtype for p in (gamma, beta) if p is not None), x.dtype)
-    allowed = (x.dtype, torch.float32)
-    g = _vector(gamma, "gamma", N, allowed, dev)
-    b = _vector(beta, "beta", N, (pdt,), dev)
-    o = list(out) if out is not None else [None] * 3
-    y = torch.empty((M, N), dtype=x.dtype, device=dev) if o[0] is None else o[0]
-    mean = torch.empty(M, dtype=torch.float32, device=dev) if o[1] is None else o[1]
-    rstd = torch.empty(M, dtype=torch.float32, device=dev) if o[2] is None else o[2]
-    _run(dev, "fp8bq_layernorm_forward", x.data_ptr(), M, N, ldx, g, b, float(eps), y.data_ptr(),
-         _rows(y, "y", (M, N), x.dtype, dev), _vector(mean, "mean", M, (torch.float32,), dev),
-         _vector(rstd, "rstd", M, (torch.float32,), dev), code, _ROW_DTYPES.get(pdt, 0))
+    device = x.get_device()
+    g = b = None
+    pdt = x.dtype
+    if gamma is not None:
+        pdt = gamma.dtype
+        g = _vector(gamma, "gamma", N, (x.dtype, _F32), device)
+    if beta is not None:
+        pdt = pdt if gamma is not None else beta.dtype
+        b = _vector(beta, "beta", N, (pdt,) if gamma is not None else (x.dtype, _F32), device)
+    y, mean, rstd = out if out is not None else (None, None, None)
+    if y is None:
+        y = _new_rows(x)
+    mean = x.new_empty(M, dtype=_F32) if mean is None else mean
+    rstd = x.new_empty(M, dtype=_F32) if rstd is None else rstd
+    _run(device, "fp8bq_layernorm_forward", x.data_ptr(), M, N, ldx, g, b, eps, y.data_ptr(), _rows_like(y, "y", x),
+         _vector(mean, "mean", M, (_F32,), device), _vector(rstd, "rstd", M, (_F32,), device), code, _ROW_DTYPES[pdt])
     return y, mean, rstd
 
 
@@ -675,34 +710,35 @@ NORM_RSTD_F64 = 2
 
 
 def _norm_backward(what, dy, x, mean, rstd, gamma, dres, params, out, accumulate):
-    code, ldx = _row_dtype(x, "x"), _rows(x, "x")
+    code, ldx = _rows(x, "x")
     M, N = x.shape
-    dev, layernorm = x.device, what == "fp8bq_layernorm_backward"
-    lddy = _rows(dy, "dy", (M, N), x.dtype, dev)
-    lddres = _rows(dres, "dres", (M, N), x.dtype, dev) if dres is not None else 0
-    g = _vector(gamma, "gamma", N, (x.dtype, torch.float32), dev)
-    o = list(out) if out is not None else [None] * 3
-    dx = torch.empty((M, N), dtype=x.dtype, device=dev) if o[0] is None else o[0]
-    dgamma = dbeta = None
-    n, ws = 0, None
+    device, layernorm = x.get_device(), what == "fp8bq_layernorm_backward"
+    f32 = (_F32,)
+    lddy = _rows_like(dy, "dy", x)
+    dx, dgamma, dbeta = out if out is not None else (None, None, None)
+    if dx is None:
+        dx = _new_rows(x)
+    pg = pb = pw = None
+    n = 0
     if params:
-        if accumulate and (o[1] is None or (layernorm and o[2] is None)):
+        if accumulate and (dgamma is None or (layernorm and dbeta is None)):
             raise ValueError("accumulate=True needs the tensors to add into")
-        dgamma = torch.empty(N, dtype=torch.float32, device=dev) if o[1] is None else o[1]
+        dgamma = x.new_empty(N, dtype=_F32) if dgamma is None else dgamma
+        pg = _vector(dgamma, "dgamma", N, f32, device)
         if layernorm:
-            dbeta = torch.empty(N, dtype=torch.float32, device=dev) if o[2] is None else o[2]
-        n = _workspace_bytes(dev, "fp8bq_norm_workspace_bytes", M, N)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    f32 = (torch.float32,)
+            dbeta = x.new_empty(N, dtype=_F32) if dbeta is None else dbeta
+            pb = _vector(dbeta, "dbeta", N, f32, device)
+        ws, pw, n = _workspace(device, x, "fp8bq_norm_workspace_bytes", M, N)
+    else:
+        dgamma = dbeta = None
     args = _CNormGrad(dy.data_ptr(), x.data_ptr(), None if dres is None else dres.data_ptr(), dx.data_ptr(), M, N, lddy, ldx,
-                      lddres, _rows(dx, "dx", (M, N), x.dtype, dev), g,
-                      _vector(mean, "mean", M, f32, dev) if layernorm else None,
-                      _vector(rstd, "rstd", M, (torch.float32, torch.float64), dev),
-                      _vector(dgamma, "dgamma", N, f32, dev), _vector(dbeta, "dbeta", N, f32, dev),
-                      None if ws is None else ws.data_ptr(), n, code,
+                      0 if dres is None else _rows_like(dres, "dres", x), _rows_like(dx, "dx", x),
+                      None if gamma is None else _vector(gamma, "gamma", N, (x.dtype, _F32), device),
+                      _vector(mean, "mean", M, f32, device) if layernorm else None,
+                      _vector(rstd, "rstd", M, (_F32, torch.float64), device), pg, pb, pw, n, code,
                       code if gamma is None else _ROW_DTYPES[gamma.dtype],
                       (NORM_ACCUMULATE if accumulate else 0) | (NORM_RSTD_F64 if rstd.dtype == torch.float64 else 0), 0)
-    _run(dev, what, ctypes.byref(args))
+    _run(device, what, args)
     return dx, dgamma, dbeta
 
 
@@ -738,34 +774,33 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _grad_table(grads, out):
-    table = (_CGrad * max(1, len(grads)))()
-    dev = None
+def _grad_call(what, grads, out, *more):
+    count = len(grads)
+    if count == 0:
+        raise ValueError("no gradients")
+    if out is not None and len(out) != count:
+        raise ValueError("as many outputs as gradients")
+    device = grads[0].get_device()
+    fields = []
     for i, g in enumerate(grads):
-        code = _row_dtype(g, "a gradient")
-        if dev is None:
-            dev = g.device
-        if not g.is_cuda or g.device != dev:
-            raise ValueError("the gradients must be on one CUDA device")
+        code = _ROW_DTYPES.get(g.dtype)
+        if code is None or g.get_device() != device or device < 0:
+            raise ValueError("the gradients must be bf16, fp16 or fp32 tensors on one CUDA device")
         if not _dense(g):
             raise ValueError("a gradient must fill one span of memory")
-        o = g if out is None else out[i]
-        if o is not g and (o.shape != g.shape or o.stride() != g.stride() or o.device != dev):
-            raise ValueError("each output must have its gradient's shape, strides and device")
-        table[i] = (g.data_ptr(), o.data_ptr(), g.numel(), code, _row_dtype(o, "an output"))
-    return table, dev
-
-
-def _grad_call(what, grads, out, *more):
-    if len(grads) == 0:
-        raise ValueError("no gradients")
-    if out is not None and len(out) != len(grads):
-        raise ValueError("as many outputs as gradients")
-    table, dev = _grad_table(grads, out)
-    n = _workspace_bytes(dev, "fp8bq_grad_workspace_bytes", len(grads))
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    _run(dev, what, table, len(grads), *more, norm.data_ptr(), ws.data_ptr(), n)
+        p = g.data_ptr()
+        if out is None:
+            fields += (p, p, g.numel(), code | code << 32)
+            continue
+        o = out[i]
+        ocode = _ROW_DTYPES.get(o.dtype)
+        if ocode is None or o.shape != g.shape or o.get_device() != device or o.stride() != g.stride():
+            raise ValueError("each output must be bf16, fp16 or fp32 of its gradient's shape, strides and device")
+        fields += (p, o.data_ptr(), g.numel(), code | ocode << 32)
+    table = (ctypes.c_int64 * len(fields))(*fields)  # an array of fp8bq_grad
+    ws, pw, n = _workspace(device, grads[0], "fp8bq_grad_workspace_bytes", count)
+    norm = grads[0].new_empty((), dtype=_F32)
+    _run(device, what, ctypes.cast(table, ctypes.POINTER(_CGrad)), count, *more, norm.data_ptr(), pw, n)
     return norm
 
 
@@ -779,7 +814,7 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     """Scales a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or into the
     list `out` (same shapes; bf16, fp16 or fp32 each), and returns their global norm before
     clipping (fp32 scalar on the device)."""
-    return _grad_call("fp8bq_grad_clip", grads, out, float(max_norm))
+    return _grad_call("fp8bq_grad_clip", grads, out, max_norm)
 
 
 def set_clock_counters(counters: Optional[torch.Tensor]) -> None:

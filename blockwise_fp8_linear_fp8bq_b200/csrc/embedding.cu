@@ -381,6 +381,99 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p) {
   }
 }
 
+// ---------------------------------------------------------- few tokens --
+// One launch and no workspace: a block for each token, which sums the rows of
+// all tokens with its id unless an earlier token has it, and blocks that write
+// zeros to the rows no token names.  Every block finds its tokens by reading
+// all the ids, so this is for few of them.
+constexpr int kFewTokens = 1024;
+constexpr int64_t kFewBytes = int64_t{128} << 20;  // of a dense gradient: beyond, the ids' repeated reading shows
+constexpr int kFewRows = 1024;                     // rows a block of zeros takes at most
+
+struct FewParams {
+  GradParams g;
+  ZeroParams z;
+  const void* ids;
+  int64_t padding;
+  int* status;
+  bool i64;
+};
+
+template <class T, class G, int VEC>
+__global__ void __launch_bounds__(256) grad_few_kernel(const FewParams p) {
+  __shared__ int list[kFewTokens], counts[8];
+  __shared__ uint8_t named[kFewRows];
+  const GradParams& g = p.g;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T_ = static_cast<int>(g.T);
+  if (blockIdx.x >= static_cast<unsigned>(T_)) {
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x - T_) * p.z.rows, v1 = min(v0 + p.z.rows, p.z.V);
+    for (int i = tid; i < v1 - v0; i += 256) named[i] = 0;
+    __syncthreads();
+    bool any = false;
+    for (int i = tid; i < T_; i += 256) {
+      const int64_t id = load_id(p.ids, p.i64, i);
+      if (id >= v0 && id < v1 && id != p.padding) {
+        named[id - v0] = 1;
+        any = true;
+      }
+    }
+    if (!__syncthreads_or(any) && p.z.row_bytes == p.z.ld_bytes) {
+      zero_span(p.z.dw + v0 * p.z.row_bytes, (v1 - v0) * p.z.row_bytes, tid, 256);
+    } else {
+      for (int64_t v = v0 + warp; v < v1; v += 8)
+        if (!named[v - v0]) zero_span(p.z.dw + v * p.z.ld_bytes, p.z.row_bytes, lane, 32);
+    }
+    return;
+  }
+  const int t = static_cast<int>(blockIdx.x);
+  const int64_t id = load_id(p.ids, p.i64, t);
+  if (id < 0 || id >= g.V) {
+    if (tid == 0) atomicCAS(p.status, 0, kStatusIndex);
+    return;
+  }
+  if (id == p.padding) return;
+  // the tokens with this id, in order: 256 at a time, counted by warp
+  bool earlier = false;
+  int found = 0;
+  for (int i0 = 0; i0 < T_; i0 += 256) {
+    const int i = i0 + tid;
+    const bool same = i < T_ && load_id(p.ids, p.i64, i) == id;
+    earlier |= same && i < t;
+    const unsigned ballot = __ballot_sync(0xffffffffu, same);
+    if (lane == 0) counts[warp] = __popc(ballot);
+    __syncthreads();
+    int before = found;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += counts[w];
+      found += counts[w];
+    }
+    if (same) list[before + __popc(ballot & ((1u << lane) - 1u))] = i;
+    __syncthreads();
+  }
+  if (__syncthreads_or(earlier)) return;
+  constexpr int kBatch = 8;
+  for (int c = tid * VEC; c < g.D; c += 256 * VEC) {
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    for (int k0 = 0; k0 < found; k0 += kBatch) {
+      Pack<T, VEC> v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < found) load_pack(v[k], static_cast<const T*>(g.dy) + list[k0 + k] * g.lddy + c);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < found) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] += v[k].f(i);
+        }
+    }
+    write_row<G, VEC>(g, id, c, acc);
+  }
+}
+
+bool few_tokens(int64_t T, int64_t V, int64_t D) { return T > 0 && T <= kFewTokens && V * D * 4 <= kFewBytes; }
+
 // Tokens a chunk: few enough that short batches fill the GPU, and at most
 // about a thousand chunks, whose partial sums are the workspace.
 int chunk_tokens(int64_t T) {
@@ -407,10 +500,30 @@ cudaError_t run_grad(GradParams p, cudaStream_t stream) {
 }
 
 template <class T, class G>
-cudaError_t grad_of_type(const GradParams& p, cudaStream_t stream) {
+cudaError_t grad_of_type(const FewParams& f, bool few, cudaStream_t stream) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  const GradParams& p = f.g;
   const bool wide = p.D % kVec == 0 && rows_aligned(p.dy, p.lddy, sizeof(T), 16) && rows_aligned(p.dw, p.lddw, sizeof(G), 16);
-  return wide ? run_grad<T, G, kVec>(p, stream) : run_grad<T, G, 1>(p, stream);
+  if (!few) return wide ? run_grad<T, G, kVec>(p, stream) : run_grad<T, G, 1>(p, stream);
+  const int64_t zeros = p.accumulate ? 0 : (f.z.V + f.z.rows - 1) / f.z.rows;
+  const unsigned blocks = static_cast<unsigned>(p.T + zeros);
+  if (wide)
+    grad_few_kernel<T, G, kVec><<<blocks, 256, 0, stream>>>(f);
+  else
+    grad_few_kernel<T, G, 1><<<blocks, 256, 0, stream>>>(f);
+  return cudaGetLastError();
+}
+
+cudaError_t grad_of_types(const FewParams& f, int dtype, int dw_dtype, bool few, cudaStream_t stream) {
+  switch (dtype) {
+    case FP8BQ_BF16:
+      return dw_dtype == FP8BQ_FP32 ? grad_of_type<__nv_bfloat16, float>(f, few, stream)
+                                    : grad_of_type<__nv_bfloat16, __nv_bfloat16>(f, few, stream);
+    case FP8BQ_FP16:
+      return dw_dtype == FP8BQ_FP32 ? grad_of_type<__half, float>(f, few, stream)
+                                    : grad_of_type<__half, __half>(f, few, stream);
+    default: return grad_of_type<float, float>(f, few, stream);
+  }
 }
 
 }  // namespace
@@ -427,8 +540,8 @@ cudaError_t launch_embedding_fwd(const EmbeddingFwd& a, cudaStream_t stream) {
   }
 }
 
-int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D) {
-  if (T == 0) return 0;
+int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D, int64_t V) {
+  if (T == 0 || few_tokens(T, V, D)) return 0;
   const int64_t chunks = (T + chunk_tokens(T) - 1) / chunk_tokens(T);
   return 2 * round256(T * static_cast<int64_t>(sizeof(Token))) + chunks * 2 * D * static_cast<int64_t>(sizeof(float));
 }
@@ -438,9 +551,30 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
   cudaError_t e = device_status_word(&status);
   if (e != cudaSuccess) return e;
   const int64_t size = a.dw_dtype == FP8BQ_FP32 ? 4 : 2;
-  SortParams s{};
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int64_t tokens_bytes = round256(a.T * static_cast<int64_t>(sizeof(Token)));
+  FewParams f{};
+  GradParams& g = f.g;
+  g.tokens = reinterpret_cast<Token*>(ws);
+  g.dy = a.dy;
+  g.dw = a.dw;
+  g.T = a.T;
+  g.V = a.V;
+  g.lddy = a.lddy;
+  g.lddw = a.lddw;
+  g.D = static_cast<int>(a.D);
+  g.scale = a.scale;
+  g.accumulate = a.accumulate;
+  f.z = ZeroParams{static_cast<uint8_t*>(a.dw), a.V, a.D * size, a.lddw * size, 0};
+  f.z.rows = std::min<int64_t>(kFewRows, std::max<int64_t>(1, kZeroBytes / f.z.row_bytes));
+  if (few_tokens(a.T, a.V, a.D)) {
+    f.ids = a.ids;
+    f.padding = a.padding;
+    f.status = status;
+    f.i64 = a.ids_i64;
+    return grad_of_types(f, a.dtype, a.dw_dtype, true, stream);
+  }
+  SortParams s{};
   s.ids = a.ids;
   s.buf[0] = reinterpret_cast<Token*>(ws);
   s.buf[1] = reinterpret_cast<Token*>(ws + tokens_bytes);
@@ -476,36 +610,16 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, sort_kernel, s);
   if (e != cudaSuccess) return e;
   if (!a.accumulate) {
-    ZeroParams z{static_cast<uint8_t*>(a.dw), a.V, a.D * size, a.lddw * size, 0};
-    z.rows = std::max<int64_t>(1, kZeroBytes / z.row_bytes);
-    const int64_t blocks = std::max<int64_t>(1, (a.V + z.rows - 1) / z.rows);
+    const int64_t blocks = std::max<int64_t>(1, (a.V + f.z.rows - 1) / f.z.rows);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch_dependent(zero_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, z);
+    e = launch_dependent(zero_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, f.z);
     if (e != cudaSuccess) return e;
   }
   if (a.T == 0) return cudaSuccess;
-  GradParams g{};
-  g.tokens = s.buf[0];
-  g.dy = a.dy;
-  g.dw = a.dw;
   g.partial = reinterpret_cast<float*>(ws + 2 * tokens_bytes);
-  g.T = a.T;
-  g.V = a.V;
-  g.lddy = a.lddy;
-  g.lddw = a.lddw;
   g.chunk = chunk_tokens(a.T);
   g.chunks = (a.T + g.chunk - 1) / g.chunk;
-  g.D = static_cast<int>(a.D);
-  g.scale = a.scale;
-  g.accumulate = a.accumulate;
-  switch (a.dtype) {
-    case FP8BQ_BF16:
-      return a.dw_dtype == FP8BQ_FP32 ? grad_of_type<__nv_bfloat16, float>(g, stream)
-                                      : grad_of_type<__nv_bfloat16, __nv_bfloat16>(g, stream);
-    case FP8BQ_FP16:
-      return a.dw_dtype == FP8BQ_FP32 ? grad_of_type<__half, float>(g, stream) : grad_of_type<__half, __half>(g, stream);
-    default: return grad_of_type<float, float>(g, stream);
-  }
+  return grad_of_types(f, a.dtype, a.dw_dtype, false, stream);
 }
 
 }  // namespace fp8bq

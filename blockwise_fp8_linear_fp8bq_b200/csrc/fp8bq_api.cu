@@ -143,8 +143,8 @@ int norm_backward(const fp8bq_norm_grad* a, bool layernorm, cudaStream_t stream)
     int sms = 0;
     const cudaError_t err = fp8bq::device_sm_count(&sms);
     if (err != cudaSuccess) return cuda_status(err);
-    if (!b.workspace || b.workspace_bytes < fp8bq::norm_bwd_workspace_bytes(b.M, b.N, sms))
-      return FP8BQ_ERR_INVALID_ARG;
+    const int64_t need = fp8bq::norm_bwd_workspace_bytes(b.M, b.N, sms);
+    if (need > 0 && (!b.workspace || b.workspace_bytes < need)) return FP8BQ_ERR_INVALID_ARG;
   }
   return cuda_status(fp8bq::launch_norm_bwd(b, layernorm, stream));
 }
@@ -452,16 +452,16 @@ int fp8bq_embedding_backward(const void* dy, int64_t T, int64_t D, int64_t lddy,
   const bool accumulate = (flags & FP8BQ_EMBEDDING_ACCUMULATE) != 0;
   if (D == 0 || (T == 0 && (accumulate || V == 0))) return FP8BQ_OK;
   if ((!dw && V > 0) || (T > 0 && (!dy || !ids))) return FP8BQ_ERR_INVALID_ARG;
-  if (T > 0 && (!workspace || workspace_bytes < fp8bq::embedding_bwd_workspace_bytes(T, D)))
-    return FP8BQ_ERR_INVALID_ARG;
+  const int64_t need = fp8bq::embedding_bwd_workspace_bytes(T, D, V);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP8BQ_ERR_INVALID_ARG;
   if ((st = device_ok()) != FP8BQ_OK) return st;
   const fp8bq::EmbeddingBwd a{dy,   ids,  dw,         workspace, T, D, lddy, V, lddw, padding_id, scale,
                               dtype, dw_dtype, ids_i64 != 0, accumulate};
   return cuda_status(fp8bq::launch_embedding_bwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D) {
-  return valid_rows(T, D) ? fp8bq::embedding_bwd_workspace_bytes(T, D) : -1;
+int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D, int64_t V) {
+  return valid_rows(T, D) && valid_rows(V, D) ? fp8bq::embedding_bwd_workspace_bytes(T, D, V) : -1;
 }
 
 int fp8bq_layernorm_forward(const void* x, int64_t M, int64_t N, int64_t ldx, const void* gamma, const void* beta,

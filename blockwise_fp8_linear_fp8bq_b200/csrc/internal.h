@@ -98,7 +98,7 @@ cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream
 int64_t norm_bwd_workspace_bytes(int64_t M, int64_t N, int sms);
 cudaError_t launch_embedding_fwd(const EmbeddingFwd& a, cudaStream_t stream);
 cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream);
-int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D);
+int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D, int64_t V);
 // The norm of the listed gradients, and with `clip` their scaled copies.
 cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm, bool clip, float* norm,
                              void* workspace, cudaStream_t stream);

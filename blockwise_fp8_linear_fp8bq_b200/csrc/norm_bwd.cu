@@ -7,7 +7,10 @@
 // FP32 arithmetic, dx rounded once.  Bound by HBM: x, dy and dres are read
 // once, through a ring of rows in shared memory.  A thread keeps its columns
 // for the whole launch, their dgamma and dbeta in registers; the blocks' sums
-// go to the workspace and are added in a fixed order by a second kernel.
+// go to the workspace and are added in a fixed order by a second kernel.  Few
+// rows (small_batch) leave those sums to further blocks of the same launch,
+// which read x and dy again, from L2: one launch instead of two, and no
+// workspace.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -29,6 +32,10 @@ struct BwdParams {
   const float* mean;
   const void* rstd;
   float* partial;  // [blocks][LN ? 2 : 1][N] sums of dgamma, dbeta, or NULL
+  float* dgamma;   // few rows: written by the column blocks; either may be NULL
+  float* dbeta;
+  int row_blocks;  // the blocks that take rows; the others take columns
+  bool accumulate, in_place;  // in_place: dx overlaps x or dy
   int64_t M, N, lddy, ldx, lddres, lddx;
   float inv_n;
   bool p32, rstd64;
@@ -37,6 +44,63 @@ struct BwdParams {
 
 __device__ __forceinline__ float load_rstd(const BwdParams& p, int64_t row) {
   return p.rstd64 ? static_cast<float>(static_cast<const double*>(p.rstd)[row]) : static_cast<const float*>(p.rstd)[row];
+}
+
+__device__ __forceinline__ void write_sum(float* out, int64_t c, float s, bool accumulate) {
+  if (out != nullptr) out[c] = accumulate ? out[c] + s : s;
+}
+
+// Few rows: the sums over rows of one block's slice of columns, 8 lanes of W
+// columns (ALIGNED: four rows a warp at a time) or 32 lanes of one.
+constexpr int kSliceFloats = 2 * 64 * 64;  // of shared memory
+
+template <class T, bool LN, bool ALIGNED>
+__device__ __forceinline__ void column_block(const BwdParams& p, float* join) {
+  constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 1, kLanes = ALIGNED ? 8 : 32, kSlice = kLanes * W;
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x % kLanes, strip = threadIdx.x / kLanes, strips = blockDim.x / kLanes;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - p.row_blocks) * kSlice, c = c0 + lane * W;
+  float dg[W], db[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) dg[i] = db[i] = 0.0f;
+  if (c < p.N) {
+    for (int64_t row = strip; row < p.M; row += kBatch * strips) {
+      Pack<T, W> x[kBatch], y[kBatch];
+      float mean[kBatch], rstd[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t r = row + k * strips;
+        if (r < p.M) {
+          load_pack(x[k], static_cast<const T*>(p.x) + r * p.ldx + c);
+          load_pack(y[k], static_cast<const T*>(p.dy) + r * p.lddy + c);
+          mean[k] = LN ? p.mean[r] : 0.0f;
+          rstd[k] = load_rstd(p, r);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (row + k * strips < p.M) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            dg[i] = fmaf(y[k].f(i), (x[k].f(i) - mean[k]) * rstd[k], dg[i]);
+            db[i] += y[k].f(i);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    join[strip * kSlice + lane * W + i] = dg[i];
+    join[(strips + strip) * kSlice + lane * W + i] = db[i];
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < (LN ? 2 : 1) * kSlice; k += blockDim.x) {
+    const int which = k / kSlice, col = k - which * kSlice;
+    if (c0 + col >= p.N) continue;
+    float s = 0.0f;
+    for (int w = 0; w < strips; ++w) s += join[(which * strips + w) * kSlice + col];
+    write_sum(which == 0 ? p.dgamma : p.dbeta, c0 + col, s, p.accumulate);
+  }
 }
 
 // tpr threads a row, COLS columns each, R rows a thread between two barriers;
@@ -51,6 +115,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
   using Cols = Group<T, W, ALIGNED, FULL>;
   using Sums = Group<float, W, ALIGNED, FULL>;
   extern __shared__ __align__(128) uint8_t smem[];
+  if (blockIdx.x >= static_cast<unsigned>(p.row_blocks)) {
+    column_block<T, LN, ALIGNED>(p, reinterpret_cast<float*>(smem));
+    return;
+  }
   __shared__ float red[2][16][K];
   __shared__ __align__(8) uint64_t bars[kMostStages];
   __shared__ int abort_flag;
@@ -59,7 +127,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
   const int group = tid / tpr, t = tid - group * tpr;
   const int warps = tpr >> 5, warp0 = group * warps;
   const int n = rp.n;
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * rp.rows;
+  const int64_t row_step = static_cast<int64_t>(p.row_blocks) * rp.rows;
   int64_t block_row = static_cast<int64_t>(blockIdx.x) * rp.rows;
   RowRing<T, RES ? 3 : 2, ALIGNED> ring(rp, smem, bars, &abort_flag, block_row, row_step);
   ring.init(tid == 0);
@@ -265,6 +333,11 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(const BwdParams p) {
     dg = fmaf(d, (xv - (LN ? p.mean[row] : 0.0f)) * load_rstd(p, row), dg);
     db += d;
   }
+  if (p.partial == nullptr) {  // few rows: one block a column
+    write_sum(p.dgamma, c, dg, p.accumulate);
+    if (LN) write_sum(p.dbeta, c, db, p.accumulate);
+    return;
+  }
   float* out = p.partial + static_cast<int64_t>(blockIdx.y) * (LN ? 2 : 1) * p.N;
   out[c] = dg;
   if (LN) out[p.N + c] = db;
@@ -311,15 +384,32 @@ int64_t long_blocks(int64_t M, int64_t N, int sms) {
   return std::min<int64_t>(M, std::max<int64_t>(1, 4 * sms / ((N + 255) / 256)));
 }
 
+// Few rows: their sums are taken from L2 in the same launch.  (At [509, 2048]
+// BF16 a second launch costs the host about 4 us and its workspace 3 more; the
+// column blocks run beside the others.)
+bool small_batch(int64_t M, int64_t N) { return M <= 1024 && M * N <= int64_t{1} << 22; }
+
 template <class T, int COLS, int R, bool LN, bool RES, bool ALIGNED, bool FULL>
 cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
   p.tpr = b.tpr;
+  p.row_blocks = static_cast<int>(b.blocks);
+  const int64_t slice = ALIGNED ? 128 / static_cast<int64_t>(sizeof(T)) : 32;
+  const bool columns = p.dgamma != nullptr || p.dbeta != nullptr;
+  const int64_t slices = columns ? (p.N + slice - 1) / slice : 0;
   const auto kern = norm_bwd_kernel<T, COLS, R, LN, RES, ALIGNED, FULL>;
   const int64_t smem = std::max<int64_t>(static_cast<int64_t>(b.ring.stage_bytes) * b.ring.stages,
-                                         b.groups > 1 ? p.N * (LN ? 8 : 4) : 0);
+                                         std::max<int64_t>(b.groups > 1 ? p.N * (LN ? 8 : 4) : 0,
+                                                           columns ? kSliceFloats * 4 : 0));
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(b.blocks), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+  if (columns && p.in_place) {  // the columns are summed before dx is written over them
+    BwdParams q = p;
+    q.row_blocks = 0;
+    kern<<<static_cast<unsigned>(slices), b.tpr * b.groups, smem, stream>>>(q, b.ring);
+    kern<<<static_cast<unsigned>(b.blocks), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+  } else {
+    kern<<<static_cast<unsigned>(b.blocks + slices), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+  }
   return cudaGetLastError();
 }
 
@@ -356,7 +446,7 @@ cudaError_t run_plan(const BwdParams& p, const RowPlan& b, cudaStream_t stream) 
 template <class T, bool LN>
 cudaError_t bwd_of_type(const BwdParams& p, RowPlan& b, bool aligned, int64_t blocks, cudaStream_t stream) {
   if (b.cols == 0) {
-    if (p.partial != nullptr) {  // before dx, which may be written over dy or x
+    if (p.partial != nullptr || p.dgamma != nullptr || p.dbeta != nullptr) {  // before dx, which may be written over dy or x
       const dim3 grid(static_cast<unsigned>((p.N + 255) / 256), static_cast<unsigned>(blocks));
       norm_cols_kernel<T, LN><<<grid, 256, 0, stream>>>(p);
       const cudaError_t e = cudaGetLastError();
@@ -371,7 +461,7 @@ cudaError_t bwd_of_type(const BwdParams& p, RowPlan& b, bool aligned, int64_t bl
 }  // namespace
 
 int64_t norm_bwd_workspace_bytes(int64_t M, int64_t N, int sms) {
-  if (M == 0 || N == 0) return 0;
+  if (M == 0 || N == 0 || small_batch(M, N)) return 0;
   int64_t most = long_blocks(M, N, sms);
   for (int64_t size : {2, 4})
     for (int tensors : {2, 3})
@@ -387,16 +477,23 @@ cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream
   if (e == cudaSuccess) e = device_status_word(&status);
   if (e != cudaSuccess) return e;
   const bool sums = a.dgamma != nullptr || a.dbeta != nullptr;
+  const bool few = a.M > 0 && small_batch(a.M, a.N);
+  const bool accumulate = (a.flags & FP8BQ_NORM_ACCUMULATE) != 0;
   int64_t blocks = 0;
   if (a.M > 0) {
     const int64_t size = a.dtype == FP8BQ_FP32 ? 4 : 2;
     const bool res = a.dres != nullptr;
+    const auto overlap = [&](const void* p, int64_t ldp, const void* q, int64_t ldq) {
+      const uintptr_t pa = reinterpret_cast<uintptr_t>(p), qa = reinterpret_cast<uintptr_t>(q);
+      const auto span = [&](int64_t ld) { return static_cast<uintptr_t>(((a.M - 1) * ld + a.N) * size); };
+      return pa < qa + span(ldq) && qa < pa + span(ldp);
+    };
     const bool aligned = (a.N * size) % 16 == 0 && rows_aligned(a.x, a.ldx, size, 16) &&
                          rows_aligned(a.dy, a.lddy, size, 16) && rows_aligned(a.dx, a.lddx, size, 16) &&
                          (!res || rows_aligned(a.dres, a.lddres, size, 16)) && rows_aligned(a.gamma, 0, 1, 16);
     const bool packed = a.ldx == a.N && a.lddy == a.N && (!res || a.lddres == a.N);
     RowPlan b = plan_bwd(a.M, a.N, size, res ? 3 : 2, aligned, packed, sms);
-    blocks = b.cols != 0 ? b.blocks : long_blocks(a.M, a.N, sms);
+    blocks = b.cols != 0 ? b.blocks : few ? 1 : long_blocks(a.M, a.N, sms);
     b.ring.src[0] = a.x;
     b.ring.src[1] = a.dy;
     b.ring.src[2] = a.dres;
@@ -404,8 +501,10 @@ cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream
     b.ring.ld[1] = a.lddy;
     b.ring.ld[2] = a.lddres;
     b.ring.status = status;
-    const BwdParams p{a.dy, a.x, a.dres, a.dx, a.gamma, a.mean, a.rstd, sums ? static_cast<float*>(a.workspace) : nullptr,
-                      a.M, a.N, a.lddy, a.ldx, a.lddres, a.lddx, 1.0f / static_cast<float>(a.N),
+    const BwdParams p{a.dy, a.x, a.dres, a.dx, a.gamma, a.mean, a.rstd,
+                      sums && !few ? static_cast<float*>(a.workspace) : nullptr, few ? a.dgamma : nullptr,
+                      few && layernorm ? a.dbeta : nullptr, 0, accumulate,
+                      overlap(a.dx, a.lddx, a.x, a.ldx) || overlap(a.dx, a.lddx, a.dy, a.lddy), a.M, a.N, a.lddy, a.ldx, a.lddres, a.lddx, 1.0f / static_cast<float>(a.N),
                       a.param_dtype == FP8BQ_FP32, (a.flags & FP8BQ_NORM_RSTD_F64) != 0, 0};
     switch (a.dtype) {
       case FP8BQ_BF16:
@@ -422,11 +521,11 @@ cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream
     }
     if (e != cudaSuccess) return e;
   }
-  if (!sums) return cudaSuccess;
+  if (!sums || few) return cudaSuccess;
   const int64_t width = a.N * (layernorm ? 2 : 1);
   return launch_dependent(norm_param_grad_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(512), 0, stream,
                           static_cast<const float*>(a.workspace), blocks, width, a.N, a.dgamma,
-                          layernorm ? a.dbeta : nullptr, (a.flags & FP8BQ_NORM_ACCUMULATE) != 0);
+                          layernorm ? a.dbeta : nullptr, accumulate);
 }
 
 }  // namespace fp8bq

@@ -293,7 +293,8 @@ int fp8bq_embedding_forward(const void* w, int64_t V, int64_t D, int64_t ldw, co
  *   flags       0, or FP8BQ_EMBEDDING_ACCUMULATE: dW += the sum (FP32 master
  *               gradients), each value rounded once; rows no id names are
  *               then neither read nor written.
- *   workspace   fp8bq_embedding_workspace_bytes(T, D) bytes.
+ *   workspace   fp8bq_embedding_workspace_bytes(T, D, V) bytes; may be NULL when
+ *               that is 0 (few tokens).
  * An id outside [0, V) adds nothing and is reported as by the lookup.
  * Errors: as the lookup; ERR_INVALID_ARG for other flag bits, a dw_dtype
  * other than the two, or a workspace too small.
@@ -303,7 +304,7 @@ int fp8bq_embedding_backward(const void* dy, int64_t T, int64_t D, int64_t lddy,
                              float scale, int64_t padding_id, void* dw, int64_t lddw, int dtype, int dw_dtype,
                              uint32_t flags, void* workspace, int64_t workspace_bytes, fp8bq_stream_t stream);
 /* Workspace bytes of fp8bq_embedding_backward; -1 on bad arguments. */
-int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D);
+int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D, int64_t V);
 
 /*
  * LayerNorm: y = (x - mean) * rstd * gamma + beta, mean and rstd = 1 /
@@ -340,7 +341,7 @@ int fp8bq_layernorm_forward(const void* x, int64_t M, int64_t N, int64_t ldx, co
  *               dbeta).
  *   flags       0 or the two above.
  *   workspace   fp8bq_norm_workspace_bytes(M, N) bytes; may be NULL when
- *               neither dgamma nor dbeta is wanted.
+ *               that is 0 (few rows) or neither dgamma nor dbeta is wanted.
  * With M == 0, dgamma and dbeta are zeros (or left as they are); N == 0 is a
  * no-op.
  * Errors: as above; ERR_INVALID_ARG for other flag bits or a workspace too

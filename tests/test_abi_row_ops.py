@@ -45,12 +45,14 @@ def test_embedding_forward_arguments(L):
 
 
 def test_embedding_backward_arguments(L):
-    n = L.fp8bq_embedding_workspace_bytes(5, 64)
+    n = L.fp8bq_embedding_workspace_bytes(5000, 64, 100)
     assert n > 0
-    assert L.fp8bq_embedding_workspace_bytes(0, 64) == 0
-    assert L.fp8bq_embedding_workspace_bytes(-1, 64) == -1 and L.fp8bq_embedding_workspace_bytes(5, -1) == -1
+    assert L.fp8bq_embedding_workspace_bytes(0, 64, 100) == 0
+    assert L.fp8bq_embedding_workspace_bytes(-1, 64, 100) == -1 and L.fp8bq_embedding_workspace_bytes(5, -1, 100) == -1
+    assert L.fp8bq_embedding_workspace_bytes(5, 64, -1) == -1
+    assert L.fp8bq_embedding_workspace_bytes(5, 64, 100) == 0  # few tokens: none
 
-    def f(dy=P, T=5, D=64, lddy=64, ids=P, i64=1, V=100, scale=1.0, pad=-1, dw=P, lddw=64, dt=BF16, dwt=FP32, flags=0,
+    def f(dy=P, T=5000, D=64, lddy=64, ids=P, i64=1, V=100, scale=1.0, pad=-1, dw=P, lddw=64, dt=BF16, dwt=FP32, flags=0,
           ws=P, nbytes=n):
         return L.fp8bq_embedding_backward(dy, T, D, lddy, ids, i64, V, scale, pad, dw, lddw, dt, dwt, flags, ws, nbytes,
                                           None)
@@ -64,6 +66,7 @@ def test_embedding_backward_arguments(L):
     assert f(D=0, lddy=0, lddw=0) == OK
     assert f(T=0, flags=1) == OK                            # nothing to add
     assert f(T=0, dy=None, ids=None, ws=None, nbytes=0) in NODEV  # the gradient is all zeros
+    assert f(T=5, ws=None, nbytes=0) in NODEV
 
 
 def test_layernorm_forward_arguments(L):
