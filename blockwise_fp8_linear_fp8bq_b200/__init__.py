@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -181,9 +182,9 @@ def lib():
         L.fp8bq_norm_workspace_bytes.restype = i64
         L.fp8bq_norm_workspace_bytes.argtypes = [i64, i64]
         L.fp8bq_grad_norm.restype = i32
-        L.fp8bq_grad_norm.argtypes = [ctypes.POINTER(_CGrad), i32, vp, vp, i64, vp]
+        L.fp8bq_grad_norm.argtypes = [vp, i32, vp, vp, i64, vp]
         L.fp8bq_grad_clip.restype = i32
-        L.fp8bq_grad_clip.argtypes = [ctypes.POINTER(_CGrad), i32, ctypes.c_double, vp, vp, i64, vp]
+        L.fp8bq_grad_clip.argtypes = [vp, i32, ctypes.c_double, vp, vp, i64, vp]
         L.fp8bq_grad_workspace_bytes.restype = i64
         L.fp8bq_grad_workspace_bytes.argtypes = [i32]
         L.fp8bq_check.restype = i32
@@ -579,6 +580,14 @@ def _vector(t: torch.Tensor, name: str, n: int, dtypes, device: int) -> int:
     return t.data_ptr()
 
 
+def _given(t: Optional[torch.Tensor], name: str, n: int, x: torch.Tensor, device: int):
+    """An fp32 vector of n entries to write, a new one for None, and its address."""
+    if t is None:
+        t = x.new_empty(n, dtype=_F32)
+        return t, t.data_ptr()
+    return t, _vector(t, name, n, (_F32,), device)
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() without its Stream object
 
 
@@ -696,12 +705,11 @@ def layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, bet
         pdt = pdt if gamma is not None else beta.dtype
         b = _vector(beta, "beta", N, (pdt,) if gamma is not None else (x.dtype, _F32), device)
     y, mean, rstd = out if out is not None else (None, None, None)
-    if y is None:
-        y = _new_rows(x)
-    mean = x.new_empty(M, dtype=_F32) if mean is None else mean
-    rstd = x.new_empty(M, dtype=_F32) if rstd is None else rstd
-    _run(device, "fp8bq_layernorm_forward", x.data_ptr(), M, N, ldx, g, b, eps, y.data_ptr(), _rows_like(y, "y", x),
-         _vector(mean, "mean", M, (_F32,), device), _vector(rstd, "rstd", M, (_F32,), device), code, _ROW_DTYPES[pdt])
+    y, ldy = (_new_rows(x), N) if y is None else (y, _rows_like(y, "y", x))
+    mean, pm = _given(mean, "mean", M, x, device)
+    rstd, pr = _given(rstd, "rstd", M, x, device)
+    _run(device, "fp8bq_layernorm_forward", x.data_ptr(), M, N, ldx, g, b, eps, y.data_ptr(), ldy, pm, pr, code,
+         _ROW_DTYPES[pdt])
     return y, mean, rstd
 
 
@@ -716,23 +724,20 @@ def _norm_backward(what, dy, x, mean, rstd, gamma, dres, params, out, accumulate
     f32 = (_F32,)
     lddy = _rows_like(dy, "dy", x)
     dx, dgamma, dbeta = out if out is not None else (None, None, None)
-    if dx is None:
-        dx = _new_rows(x)
+    dx, lddx = (_new_rows(x), N) if dx is None else (dx, _rows_like(dx, "dx", x))
     pg = pb = pw = None
     n = 0
     if params:
         if accumulate and (dgamma is None or (layernorm and dbeta is None)):
             raise ValueError("accumulate=True needs the tensors to add into")
-        dgamma = x.new_empty(N, dtype=_F32) if dgamma is None else dgamma
-        pg = _vector(dgamma, "dgamma", N, f32, device)
+        dgamma, pg = _given(dgamma, "dgamma", N, x, device)
         if layernorm:
-            dbeta = x.new_empty(N, dtype=_F32) if dbeta is None else dbeta
-            pb = _vector(dbeta, "dbeta", N, f32, device)
+            dbeta, pb = _given(dbeta, "dbeta", N, x, device)
         ws, pw, n = _workspace(device, x, "fp8bq_norm_workspace_bytes", M, N)
     else:
         dgamma = dbeta = None
     args = _CNormGrad(dy.data_ptr(), x.data_ptr(), None if dres is None else dres.data_ptr(), dx.data_ptr(), M, N, lddy, ldx,
-                      0 if dres is None else _rows_like(dres, "dres", x), _rows_like(dx, "dx", x),
+                      0 if dres is None else _rows_like(dres, "dres", x), lddx,
                       None if gamma is None else _vector(gamma, "gamma", N, (x.dtype, _F32), device),
                       _vector(mean, "mean", M, f32, device) if layernorm else None,
                       _vector(rstd, "rstd", M, (_F32, torch.float64), device), pg, pb, pw, n, code,
@@ -781,26 +786,27 @@ def _grad_call(what, grads, out, *more):
     if out is not None and len(out) != count:
         raise ValueError("as many outputs as gradients")
     device = grads[0].get_device()
-    fields = []
-    for i, g in enumerate(grads):
+    fields = []  # of an array of fp8bq_grad
+    for g, o in zip(grads, grads if out is None else out):
         code = _ROW_DTYPES.get(g.dtype)
         if code is None or g.get_device() != device or device < 0:
             raise ValueError("the gradients must be bf16, fp16 or fp32 tensors on one CUDA device")
-        if not _dense(g):
+        plain = g.is_contiguous()
+        if not plain and not _dense(g):
             raise ValueError("a gradient must fill one span of memory")
         p = g.data_ptr()
-        if out is None:
+        if o is g:
             fields += (p, p, g.numel(), code | code << 32)
             continue
-        o = out[i]
         ocode = _ROW_DTYPES.get(o.dtype)
-        if ocode is None or o.shape != g.shape or o.get_device() != device or o.stride() != g.stride():
+        if (ocode is None or o.shape != g.shape or o.get_device() != device
+                or not (plain and o.is_contiguous() or o.stride() == g.stride())):
             raise ValueError("each output must be bf16, fp16 or fp32 of its gradient's shape, strides and device")
         fields += (p, o.data_ptr(), g.numel(), code | ocode << 32)
-    table = (ctypes.c_int64 * len(fields))(*fields)  # an array of fp8bq_grad
+    table = struct.pack(f"={len(fields)}q", *fields)
     ws, pw, n = _workspace(device, grads[0], "fp8bq_grad_workspace_bytes", count)
     norm = grads[0].new_empty((), dtype=_F32)
-    _run(device, what, ctypes.cast(table, ctypes.POINTER(_CGrad)), count, *more, norm.data_ptr(), pw, n)
+    _run(device, what, table, count, *more, norm.data_ptr(), pw, n)
     return norm
 
 

@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
                                                        const __grid_constant__ RingParams rp) {
   constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 8, G = COLS / W;
   constexpr int K = LN ? 2 * R : R;               // sums a thread takes part in
-  constexpr bool kGammaRegs = COLS <= 16;         // else read again for each row
-  using Cols = Group<T, W, ALIGNED, FULL>;
-  using Sums = Group<float, W, ALIGNED, FULL>;
+  constexpr bool kGammaRegs = COLS <= 16;         // else in shared memory, behind the ring
+  using Cols = Group<T, W, ALIGNED, FULL, (G > 2)>;
+  using Sums = Group<float, W, ALIGNED, FULL, false>;
   extern __shared__ __align__(128) uint8_t smem[];
   if (blockIdx.x >= static_cast<unsigned>(p.row_blocks)) {
     column_block<T, LN, ALIGNED>(p, reinterpret_cast<float*>(smem));
@@ -133,11 +133,38 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
   ring.init(tid == 0);
   if (warp == 0) ring.start();
 
+  // gamma: pair i of group j of thread t at [(j * W / 2 + i) * tpr + t], as FP32
+  // or T pairs, whichever it came as
+  uint8_t* const gamma_at = smem + rp.stages * rp.stage_bytes;
+  const bool wide_gamma = p.p32 || p.gamma == nullptr;
+  const auto keep_gamma = [&](int j) {
+    float2 g[W / 2];
+    Cols::load_param(g, p.gamma, p.p32, 1.0f, t, tpr, j, n);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      const int at = (j * (W / 2) + i) * tpr + t;
+      if (sizeof(T) == 4 || wide_gamma)
+        reinterpret_cast<float2*>(gamma_at)[at] = g[i];
+      else
+        from_float2(reinterpret_cast<T*>(gamma_at) + 2 * at, g[i]);
+    }
+  };
+  const auto kept_gamma = [&](float2 (&g)[W / 2], int j) {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      const int at = (j * (W / 2) + i) * tpr + t;
+      g[i] = sizeof(T) == 4 || wide_gamma ? reinterpret_cast<const float2*>(gamma_at)[at]
+                                          : to_float2(reinterpret_cast<const T*>(gamma_at) + 2 * at);
+    }
+  };
   float2 gam[kGammaRegs ? G : 1][W / 2];
   float2 dg[G][W / 2], db[G][W / 2];
 #pragma unroll
   for (int j = 0; j < G; ++j) {
-    if constexpr (kGammaRegs) Cols::load_param(gam[j], p.gamma, p.p32, 1.0f, t, tpr, j, n);
+    if constexpr (kGammaRegs)
+      Cols::load_param(gam[j], p.gamma, p.p32, 1.0f, t, tpr, j, n);
+    else
+      keep_gamma(j);  // each thread reads only what it wrote itself
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) dg[j][i] = db[j][i] = make_float2(0.0f, 0.0f);
   }
@@ -196,7 +223,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
         float2 x[W / 2], y[W / 2], gj[W / 2];
         Cols::load(x, sx, t, tpr, j, n);
         Cols::load(y, sy, t, tpr, j, n);
-        if constexpr (!kGammaRegs) Cols::load_param(gj, p.gamma, p.p32, 1.0f, t, tpr, j, n);
+        if constexpr (!kGammaRegs) kept_gamma(gj, j);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
           const float2 g = __fmul2_rn(y[i], kGammaRegs ? gam[kGammaRegs ? j : 0][i] : gj[i]);
@@ -238,7 +265,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
         Cols::load(x, sx, t, tpr, j, n);
         Cols::load(y, sy, t, tpr, j, n);
         if (RES) Cols::load(z, sr, t, tpr, j, n);
-        if constexpr (!kGammaRegs) Cols::load_param(gj, p.gamma, p.p32, 1.0f, t, tpr, j, n);
+        if constexpr (!kGammaRegs) kept_gamma(gj, j);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
           const float2 g = __fmul2_rn(y[i], kGammaRegs ? gam[kGammaRegs ? j : 0][i] : gj[i]);
@@ -369,14 +396,18 @@ __global__ void __launch_bounds__(512) norm_param_grad_kernel(const float* __res
   *out = accumulate ? *out + s : s;
 }
 
+// Shared memory for gamma.
+int64_t gamma_bytes(const RowPlan& b, int64_t size) { return b.cols > 16 ? static_cast<int64_t>(b.tpr) * b.cols * size : 0; }
+
 // As many rows between two barriers as leave the ring two stages (measured at
 // [16384, 2048] BF16 with a residual, LayerNorm, 8 columns a thread: 75 us with
 // one row, 57 with two, 51 with four).
-RowPlan plan_bwd(int64_t M, int64_t N, int64_t size, int tensors, bool aligned, bool packed, int sms) {
+RowPlan plan_bwd(int64_t M, int64_t N, int64_t size, int tensors, bool aligned, bool packed, bool wide_gamma, int sms) {
   const int least = aligned ? static_cast<int>(16 / size) : 8;
   const RowChoice choices[] = {{256, least, 4}, {256, 8, 4}, {256, 16, 2}, {512, 16, 2}, {512, 32, 1}};
   if (aligned && (N * size) % 16 != 0) return RowPlan{};
-  return plan_rows(choices, 5, M, N, size, tensors, aligned, packed, sms, [](int threads, int) { return threads > 256 ? 1 : 2; });
+  return plan_rows(choices, 5, M, N, size, tensors, aligned, packed, sms, [](int threads, int) { return threads > 256 ? 1 : 2; },
+                   [&](const RowPlan& b) { return gamma_bytes(b, wide_gamma ? 4 : size); });
 }
 
 // Rows too long for a block: the blocks that share each column's sum.
@@ -397,7 +428,8 @@ cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
   const bool columns = p.dgamma != nullptr || p.dbeta != nullptr;
   const int64_t slices = columns ? (p.N + slice - 1) / slice : 0;
   const auto kern = norm_bwd_kernel<T, COLS, R, LN, RES, ALIGNED, FULL>;
-  const int64_t smem = std::max<int64_t>(static_cast<int64_t>(b.ring.stage_bytes) * b.ring.stages,
+  const int64_t smem = std::max<int64_t>(static_cast<int64_t>(b.ring.stage_bytes) * b.ring.stages +
+                                             gamma_bytes(b, p.p32 || p.gamma == nullptr ? 4 : sizeof(T)),
                                          std::max<int64_t>(b.groups > 1 ? p.N * (LN ? 8 : 4) : 0,
                                                            columns ? kSliceFloats * 4 : 0));
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -465,8 +497,8 @@ int64_t norm_bwd_workspace_bytes(int64_t M, int64_t N, int sms) {
   int64_t most = long_blocks(M, N, sms);
   for (int64_t size : {2, 4})
     for (int tensors : {2, 3})
-      for (int how = 0; how < 4; ++how)
-        most = std::max(most, plan_bwd(M, N, size, tensors, (how & 1) != 0, (how & 2) != 0, sms).blocks);
+      for (int how = 0; how < 8; ++how)
+        most = std::max(most, plan_bwd(M, N, size, tensors, (how & 1) != 0, (how & 2) != 0, (how & 4) != 0, sms).blocks);
   return most * 2 * N * static_cast<int64_t>(sizeof(float));
 }
 
@@ -492,7 +524,8 @@ cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream
                          rows_aligned(a.dy, a.lddy, size, 16) && rows_aligned(a.dx, a.lddx, size, 16) &&
                          (!res || rows_aligned(a.dres, a.lddres, size, 16)) && rows_aligned(a.gamma, 0, 1, 16);
     const bool packed = a.ldx == a.N && a.lddy == a.N && (!res || a.lddres == a.N);
-    RowPlan b = plan_bwd(a.M, a.N, size, res ? 3 : 2, aligned, packed, sms);
+    RowPlan b = plan_bwd(a.M, a.N, size, res ? 3 : 2, aligned, packed,
+                         a.param_dtype == FP8BQ_FP32 || a.gamma == nullptr, sms);
     blocks = b.cols != 0 ? b.blocks : few ? 1 : long_blocks(a.M, a.N, sms);
     b.ring.src[0] = a.x;
     b.ring.src[1] = a.dy;

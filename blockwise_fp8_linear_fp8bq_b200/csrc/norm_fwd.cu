@@ -39,37 +39,49 @@ __device__ __forceinline__ float rstd_of(float var, float eps) {
   return __fdiv_rn(1.0f, __fsqrt_rn(fmaxf(var, 0.0f) + eps));
 }
 
-// A team of tpr threads takes a row at a time, COLS columns a thread, which
-// stay in registers from one pass to the next.  Teams share nothing but gamma
-// and beta: SHARED keeps those in shared memory, as FP32 pairs, else (the
-// longest rows, one team a block) in registers.  Few threads with many
+// A team of tpr threads takes a row at a time (SUB = 8: a team of one warp four
+// rows, 8 lanes each), COLS columns a thread, which stay in registers from one
+// pass to the next.  Teams share nothing but gamma and beta: SHARED keeps
+// those in shared memory, as FP32 pairs, else (few rows, or the longest; one
+// team a block) in registers.  Few threads with many
 // columns, because the sums over a team cost as much for one column as for
 // many: at [16384, 2048] BF16, 256-thread teams of 8 columns ran at 3.1 TB/s.
-template <class T, int COLS, bool ALIGNED, bool FULL, bool SHARED>
+template <int SUB>
+__device__ __forceinline__ float sub_sum(float v) {
+#pragma unroll
+  for (int o = SUB / 2; o >= 1; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <class T, int COLS, int SUB, bool ALIGNED, bool FULL, bool SHARED>
 __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const __grid_constant__ FwdParams p,
                                                      const __grid_constant__ RingParams rp) {
   constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 8, G = COLS / W;
+  constexpr int R = 32 / SUB;  // rows a team takes at a time
   using Cols = Group<T, W, ALIGNED, FULL>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[16][kMostStages];
   __shared__ int abort_flag;
   __shared__ float centre[2][16], sums[2][16], squares[2][16], held[16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tpr = p.tpr, team = tid / tpr, t = tid - team * tpr, teams = blockDim.x / tpr;
-  const int warps = tpr >> 5, warp0 = team * warps;
+  const int members = SUB < 32 ? 32 : p.tpr, team = tid / members, teams = blockDim.x / members;
+  const int tpr = SUB < 32 ? SUB : p.tpr, t = SUB < 32 ? lane % SUB : tid - team * members;  // threads a row
+  const int warps = members >> 5, warp0 = team * warps;
   const int n = rp.n;
 
-  const int64_t first_row = blockIdx.x + static_cast<int64_t>(gridDim.x) * team;  // rows over the SMs first
-  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  // rows over the SMs first
+  const int64_t first_row = (blockIdx.x + static_cast<int64_t>(gridDim.x) * team) * R;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams * R;
   float4* const params = reinterpret_cast<float4*>(smem);  // [COLS / 2][tpr]: a pair's gammas, its betas
   uint8_t* const rings = smem + (SHARED ? COLS / 2 * tpr * static_cast<int>(sizeof(float4)) : 0);
   RowRing<T, 1, ALIGNED> ring(rp, rings + team * rp.stages * rp.stage_bytes, bars[team], &abort_flag, first_row, step);
-  ring.init(t == 0);
+  const bool leader = tid == team * members;
+  ring.init(leader);
   if (warp == warp0) ring.start();
 
   float2 gam[SHARED ? 1 : G][W / 2], bet[SHARED ? 1 : G][W / 2];
   if constexpr (SHARED) {
-    for (int j = team; j < G; j += teams) {
+    for (int j = tid / tpr; j < G; j += blockDim.x / tpr) {
       float2 g[W / 2], b[W / 2];
       Cols::load_param(g, p.gamma, p.p32, 1.0f, t, tpr, j, n);
       Cols::load_param(b, p.beta, p.p32, 0.0f, t, tpr, j, n);
@@ -88,15 +100,16 @@ __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const _
   for (int j = 0; j < G; ++j)
 #pragma unroll
     for (int k = 0; k < W; ++k) count += FULL || Cols::column(t, tpr, j, k) < n ? 1.0f : 0.0f;
-  count = warp_sum(count);
+  count = sub_sum<SUB>(count);
   const float inv_count = count > 0.0f ? __fdiv_rn(1.0f, count) : 0.0f;
   if (lane == 0) held[warp] = count;
   __syncthreads();
 
   int buf = 0;
-  for (int64_t row = first_row; row < rp.M; row += step, buf ^= 1) {
+  for (int64_t row0 = first_row; row0 < rp.M; row0 += step, buf ^= 1) {
     ring.wait();
-    const T* x = ring.row(0, row, 0);
+    const int64_t row = row0 + (SUB < 32 ? lane / SUB : 0);
+    const T* x = ring.row(0, row0, SUB < 32 ? lane / SUB : 0);
     float2 v[G][W / 2];
     float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
 #pragma unroll
@@ -109,29 +122,26 @@ __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const _
       }
     }
     sum = __fadd2_rn(sum, sum2);
-    const float mid = warp_sum(sum.x + sum.y) * inv_count;
+    const float mid = sub_sum<SUB>(sum.x + sum.y) * inv_count;
     const float2 m2 = make_float2(-mid, -mid);
     float2 sq = make_float2(0.0f, 0.0f), sq2 = sq;
     sum = sum2 = sq;
 #pragma unroll
-    for (int j = 0; j < G; ++j)
+    for (int j = 0; j < G; ++j) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) v[j][i] = __fadd2_rn(v[j][i], m2);
+      Cols::clear_rest(v[j], t, tpr, j, n);
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
-        float2& d = v[j][i];
-        d = __fadd2_rn(d, m2);
-        if (!FULL && Cols::column(t, tpr, j, 2 * i) >= n) d.x = 0.0f;
-        if (!FULL && Cols::column(t, tpr, j, 2 * i + 1) >= n) d.y = 0.0f;
         float2& s = i % 2 ? sum2 : sum;
         float2& q = i % 2 ? sq2 : sq;
-        s = __fadd2_rn(s, d);
-        q = __ffma2_rn(d, d, q);
+        s = __fadd2_rn(s, v[j][i]);
+        q = __ffma2_rn(v[j][i], v[j][i], q);
       }
+    }
     sum = __fadd2_rn(sum, sum2);
     sq = __fadd2_rn(sq, sq2);
-    float part[2] = {sum.x + sum.y, sq.x + sq.y};
-    int index;
-    const float both = warp_sums<2>(part, lane, index);
-    float s = warp_sum_of<2>(both, 0), q = warp_sum_of<2>(both, 1);
+    const float s = sub_sum<SUB>(sum.x + sum.y), q = sub_sum<SUB>(sq.x + sq.y);
     // the row's mean is base + avg: base a rounded mean, avg what it is off by
     float base = mid, avg, var;
     if (warps > 1) {
@@ -156,7 +166,8 @@ __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const _
       var = __fdiv_rn(fmaf(-avg, s, q), p.n);
     }
     const float rstd = rstd_of(var, p.eps);
-    if (t == 0) {
+    const bool live = SUB == 32 || row < rp.M;
+    if (t == 0 && live) {
       if (p.mean != nullptr) p.mean[row] = base + avg;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
@@ -178,11 +189,11 @@ __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const _
         }
         v[j][i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j][i], a2), rs2), g, b);
       }
-      Cols::store(y, v[j], t, tpr, j, n);
+      if (live) Cols::store(y, v[j], t, tpr, j, n);
     }
     ring.next();
   }
-  ring.finish(t == 0);
+  ring.finish(leader);
 }
 
 // Rows too long for a block: read three times.
@@ -214,73 +225,96 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const FwdParams p) {
     y[c] = from_float<T>(fmaf((to_float(x[c]) - m - avg) * rstd, param(p.gamma, c, 1.0f), param(p.beta, c, 0.0f)));
 }
 
-template <class T, int COLS, bool ALIGNED, bool FULL, bool SHARED>
+template <class T, int COLS, int SUB, bool ALIGNED, bool FULL, bool SHARED>
 cudaError_t run_as(FwdParams p, const RowPlan& b, cudaStream_t stream) {
   p.tpr = b.tpr;
-  const auto kern = ln_fwd_kernel<T, COLS, ALIGNED, FULL, SHARED>;
+  const auto kern = ln_fwd_kernel<T, COLS, SUB, ALIGNED, FULL, SHARED>;
   const int smem = static_cast<int>(b.ring.stage_bytes) * b.ring.stages * b.groups + (SHARED ? b.tpr * COLS * 8 : 0);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(b.blocks), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+  kern<<<static_cast<unsigned>(b.blocks), std::max(32, b.tpr) * b.groups, smem, stream>>>(p, b.ring);
   return cudaGetLastError();
 }
 
-template <class T, int COLS, bool ALIGNED, bool SHARED>
+template <class T, int COLS, int SUB, bool ALIGNED, bool SHARED>
 cudaError_t run(const FwdParams& p, const RowPlan& b, cudaStream_t stream) {
-  if constexpr (ALIGNED)
-    if (p.N == static_cast<int64_t>(b.tpr) * COLS) return run_as<T, COLS, true, true, SHARED>(p, b, stream);
-  return run_as<T, COLS, ALIGNED, false, SHARED>(p, b, stream);
+  if constexpr (ALIGNED && SHARED)
+    if (p.N == static_cast<int64_t>(b.tpr) * COLS) return run_as<T, COLS, SUB, true, true, SHARED>(p, b, stream);
+  return run_as<T, COLS, SUB, ALIGNED, false, SHARED>(p, b, stream);
 }
 
 template <class T, bool ALIGNED>
 cudaError_t run_plan(const FwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  if (b.tpr == 8) {
+    if (b.cols == 8) return run<T, 8, 8, ALIGNED, true>(p, b, stream);
+    if (b.cols == 16) return run<T, 16, 8, ALIGNED, true>(p, b, stream);
+    return run<T, 32, 8, ALIGNED, true>(p, b, stream);
+  }
   switch (b.cols) {
-    case 8: return run<T, 8, ALIGNED, true>(p, b, stream);
-    case 16: return run<T, 16, ALIGNED, true>(p, b, stream);
-    case 32: return b.tpr == 32 ? run<T, 32, ALIGNED, true>(p, b, stream) : run<T, 32, ALIGNED, false>(p, b, stream);
-    case 48: return run<T, 48, ALIGNED, true>(p, b, stream);
-    default: return run<T, 64, ALIGNED, true>(p, b, stream);
+    case 8: return run<T, 8, 32, ALIGNED, false>(p, b, stream);
+    case 16: return run<T, 16, 32, ALIGNED, true>(p, b, stream);
+    case 32: return b.tpr == 32 ? run<T, 32, 32, ALIGNED, true>(p, b, stream) : run<T, 32, 32, ALIGNED, false>(p, b, stream);
+    case 48: return run<T, 48, 32, ALIGNED, true>(p, b, stream);
+    default: return run<T, 64, 32, ALIGNED, true>(p, b, stream);
   }
 }
 
-// Teams of one warp where 64 columns a thread hold the row, else the team and
-// columns (48 or 64) that leave the fewest idle; as many teams a block, up to
-// 16 warps, as leave each two stages.  The longest rows, whose gamma and beta
-// do not fit beside two stages, take one team of 32 columns a thread.
-RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, int sms) {
+// Few rows: a block each, 8 columns a thread (at [200, 1283] FP32 3.9 us; the
+// teams below, which first bring gamma and beta to shared memory, 6.9).
+// Rows of up to 256 columns: 8 lanes each.  Else teams of one warp where 64
+// columns a thread hold the row, or the team and columns (48 or 64) that leave
+// the fewest idle; as many teams a block, up to 16 warps, as leave each two
+// stages.  The longest rows, whose gamma and beta do not fit beside two
+// stages, take one team of 32 columns a thread.
+RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, int sms) {
   RowPlan b{};
-  const int64_t row = N * size, pitch = aligned ? row : (row + 30) / 16 * 16;
-  for (int cols : {8, 16, 32})
-    if (b.cols == 0 && N <= 32 * cols) {
-      b.cols = cols;
-      b.tpr = 32;
-    }
-  if (b.cols == 0) {
-    const auto threads = [&](int cols) { return static_cast<int>(((N + cols - 1) / cols + 31) / 32 * 32); };
+  const int64_t row = N * size;
+  const auto threads = [&](int cols) { return static_cast<int>(((N + cols - 1) / cols + 31) / 32 * 32); };
+  int64_t room = kRingBytes - kRingExtra;
+  int on_sm = 1, rows = 1;  // blocks that the registers allow; rows a team takes at a time
+  bool shared = true;
+  if (M <= 2 * sms && N <= 512 * 8) {
+    b.cols = 8;
+    b.tpr = threads(8);
+    on_sm = 2;
+    shared = false;
+  } else if (N <= 256) {
+    b.cols = N <= 64 ? 8 : N <= 128 ? 16 : 32;
+    b.tpr = 8;
+    rows = 4;
+    on_sm = b.cols <= 16 ? 2 : 1;
+  } else if (N <= 2048) {
+    b.cols = N <= 512 ? 16 : N <= 1024 ? 32 : N <= 1536 ? 48 : 64;
+    b.tpr = 32;
+    on_sm = b.cols <= 16 ? 2 : 1;
+  } else {
     b.cols = threads(48) * 48 < threads(64) * 64 ? 48 : 64;
     b.tpr = threads(b.cols);
   }
-  const int on_sm = b.cols <= 16 ? 2 : 1;  // blocks of 16 warps that the registers allow
-  int64_t room = kRingBytes / on_sm - kRingExtra - static_cast<int64_t>(b.tpr) * b.cols * 8;
-  b.groups = static_cast<int>(std::min<int64_t>(512 / b.tpr, room / (2 * pitch)));
-  int per_sm = on_sm;
+  const int64_t pitch = aligned || packed ? row : (row + 30) / 16 * 16;
+  const int64_t stage = aligned ? pitch * rows : (pitch * rows + 30) / 16 * 16;
+  room = kRingBytes / on_sm - kRingExtra - (shared ? static_cast<int64_t>(b.tpr) * b.cols * 8 : 0);
+  b.groups = static_cast<int>(std::min<int64_t>(shared ? 512 / std::max(32, b.tpr) : 1, room / (2 * stage)));
   if (b.groups < 1) {
+    if (threads(32) > 512) return RowPlan{};
     b.cols = 32;
-    b.tpr = static_cast<int>(((N + 31) / 32 + 31) / 32 * 32);
+    b.tpr = threads(32);
     b.groups = 1;
-    per_sm = 1;
+    on_sm = 1;
     room = kRingBytes - kRingExtra;
-    if (b.tpr > 512 || room < 2 * pitch) return RowPlan{};
+    if (room < 2 * stage) return RowPlan{};
   }
-  b.rows = 1;
-  b.blocks = std::min<int64_t>(M, static_cast<int64_t>(per_sm) * sms);
+  b.rows = rows;
+  const int64_t row_blocks = (M + rows - 1) / rows;
+  b.blocks = std::min<int64_t>(row_blocks, static_cast<int64_t>(on_sm) * sms);
   b.ring.M = M;
   b.ring.n = static_cast<int>(N);
-  b.ring.rows = 1;
-  b.ring.stages = static_cast<int>(std::min<int64_t>(kMostStages, room / (b.groups * pitch)));
+  b.ring.rows = rows;
+  b.ring.stages = static_cast<int>(std::min<int64_t>(shared ? kMostStages : 2, room / (b.groups * stage)));
   b.ring.row_bytes = static_cast<uint32_t>(row);
-  b.ring.pitch = b.ring.tensor_bytes = b.ring.stage_bytes = static_cast<uint32_t>(pitch);
-  b.ring.packed = false;
+  b.ring.pitch = static_cast<uint32_t>(pitch);
+  b.ring.tensor_bytes = b.ring.stage_bytes = static_cast<uint32_t>(stage);
+  b.ring.packed = packed;
   return b;
 }
 
@@ -291,7 +325,7 @@ cudaError_t fwd_of_type(const NormFwd& a, int sms, int* status, cudaStream_t str
   const bool aligned = (a.N * sizeof(T)) % 16 == 0 && rows_aligned(a.x, a.ldx, sizeof(T), 16) &&
                        rows_aligned(a.y, a.ldy, sizeof(T), 16) && rows_aligned(a.gamma, 0, 1, 16) &&
                        rows_aligned(a.beta, 0, 1, 16);
-  RowPlan b = plan_fwd(a.M, a.N, sizeof(T), aligned, sms);
+  RowPlan b = plan_fwd(a.M, a.N, sizeof(T), aligned, a.ldx == a.N, sms);
   if (b.cols == 0) {
     ln_fwd_long_kernel<T><<<static_cast<unsigned>(a.M), 1024, 0, stream>>>(p);
     return cudaGetLastError();

@@ -21,8 +21,8 @@ constexpr int kMostStages = 8;
 constexpr int kTimeoutRows = 30;
 // An SM's shared memory for the rings of its blocks, and what a block needs
 // of it beside its ring (static arrays and what the system keeps).
-constexpr int64_t kRingBytes = 224 * 1024;
-constexpr int64_t kRingExtra = 5 * 1024;
+constexpr int64_t kRingBytes = 228 * 1024;
+constexpr int64_t kRingExtra = 3 * 1024;
 
 struct RingParams {
   const void* src[3];
@@ -170,13 +170,17 @@ struct RowRing {
 
 // W columns of a row for thread t of `stride`: a pack of W = 16 bytes
 // (ALIGNED), or W values a stride apart; the j-th such group.  Pairs beyond
-// the row's n columns are zeros.  FULL: there are none.
-template <class T, int W, bool ALIGNED, bool FULL>
+// the row's n columns are zeros.  FULL: there are none.  SPLIT: groups that
+// lie within the row take code of their own, without the checks.
+template <class T, int W, bool ALIGNED, bool FULL, bool SPLIT = true>
 struct Group {
   // Column of value k.
   __device__ static __forceinline__ int column(int t, int stride, int j, int k) {
     return ALIGNED ? (t + j * stride) * W + k : t + (j * W + k) * stride;
   }
+
+  // Whether every thread's j-th group lies within the row.
+  __device__ static __forceinline__ bool whole(int stride, int j, int n) { return FULL || (SPLIT && (j + 1) * W * stride <= n); }
 
   __device__ static __forceinline__ void load(float2 (&v)[W / 2], const T* row, int t, int stride, int j, int n) {
     if constexpr (ALIGNED) {
@@ -185,12 +189,18 @@ struct Group {
       if (FULL || c < n) load_pack(x, row + c);
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) v[i] = FULL || c < n ? x.f2(i) : make_float2(0.0f, 0.0f);
+    } else if (whole(stride, j, n)) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const int c = column(t, stride, j, 2 * i);
+        v[i] = make_float2(to_float(row[c]), to_float(row[c + stride]));
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
         const int c = column(t, stride, j, 2 * i);
-        v[i].x = FULL || c < n ? to_float(row[c]) : 0.0f;
-        v[i].y = FULL || c + stride < n ? to_float(row[c + stride]) : 0.0f;
+        v[i].x = c < n ? to_float(row[c]) : 0.0f;
+        v[i].y = c + stride < n ? to_float(row[c + stride]) : 0.0f;
       }
     }
   }
@@ -203,13 +213,30 @@ struct Group {
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) o.set2(i, v[i]);
       store_pack(row + c, o);
+    } else if (whole(stride, j, n)) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const int c = column(t, stride, j, 2 * i);
+        row[c] = from_float<T>(v[i].x);
+        row[c + stride] = from_float<T>(v[i].y);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
         const int c = column(t, stride, j, 2 * i);
-        if (FULL || c < n) row[c] = from_float<T>(v[i].x);
-        if (FULL || c + stride < n) row[c + stride] = from_float<T>(v[i].y);
+        if (c < n) row[c] = from_float<T>(v[i].x);
+        if (c + stride < n) row[c + stride] = from_float<T>(v[i].y);
       }
+    }
+  }
+
+  // Zeros in the place of values past the row.
+  __device__ static __forceinline__ void clear_rest(float2 (&v)[W / 2], int t, int stride, int j, int n) {
+    if (FULL || whole(stride, j, n)) return;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      if (column(t, stride, j, 2 * i) >= n) v[i].x = 0.0f;
+      if (column(t, stride, j, 2 * i + 1) >= n) v[i].y = 0.0f;
     }
   }
 
@@ -224,7 +251,7 @@ struct Group {
         v[i].y = FULL || column(t, stride, j, 2 * i + 1) < n ? none : 0.0f;
       }
     } else if (f32) {
-      Group<float, W, ALIGNED, FULL>::load(v, static_cast<const float*>(src), t, stride, j, n);
+      Group<float, W, ALIGNED, FULL, SPLIT>::load(v, static_cast<const float*>(src), t, stride, j, n);
     } else {
       load(v, static_cast<const T*>(src), t, stride, j, n);
     }
@@ -296,10 +323,11 @@ struct RowChoice {
 };
 
 // The first choice that holds a row of N columns; `width` columns a group.
-// per_sm(threads) blocks run on an SM.
-template <class F>
+// per_sm(threads, cols) blocks run on an SM, and extra(plan) is what a block
+// needs of shared memory beside its ring.
+template <class F, class E>
 inline RowPlan plan_rows(const RowChoice* choices, int count, int64_t M, int64_t N, int64_t size, int tensors, bool aligned,
-                         bool packed, int sms, F per_sm) {
+                         bool packed, int sms, F per_sm, E extra) {
   RowPlan b{};
   for (int i = 0; i < count && b.cols == 0; ++i) {
     const RowChoice& c = choices[i];
@@ -312,7 +340,7 @@ inline RowPlan plan_rows(const RowChoice* choices, int count, int64_t M, int64_t
   if (b.cols == 0) return b;
   b.groups = std::max(1, 256 / b.tpr);
   const int on_sm = per_sm(b.tpr * b.groups, b.cols);
-  const int64_t room = kRingBytes / on_sm - kRingExtra, row = N * size;
+  const int64_t room = kRingBytes / on_sm - kRingExtra - extra(b), row = N * size;
   const int64_t pitch = aligned || packed ? row : (row + 30) / 16 * 16;
   const auto stage = [&](int rows) {
     const int64_t bytes = pitch * b.groups * rows;
