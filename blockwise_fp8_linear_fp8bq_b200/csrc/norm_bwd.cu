@@ -103,17 +103,20 @@ __device__ __forceinline__ void column_block(const BwdParams& p, float* join) {
   }
 }
 
-// tpr threads a row, COLS columns each, R rows a thread between two barriers;
-// x and dy are read from shared memory twice, before and after the row's
-// sums.  RES: dres is given.
-template <class T, int COLS, int R, bool LN, bool RES, bool ALIGNED, bool FULL>
+// tpr threads a row (SUB = 8: 8 lanes of a warp), COLS columns each, R rows a
+// thread between two barriers; x and dy are read from shared memory twice,
+// before and after the row's sums.  Aligned rows are padded there with zeros
+// to the threads' columns, so that reading them needs no checks (14-40% of
+// the time where N is not a multiple of the threads' columns).  RES: dres is
+// given.
+template <class T, int COLS, int R, int SUB, bool LN, bool RES, bool ALIGNED>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ BwdParams p,
                                                        const __grid_constant__ RingParams rp) {
   constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 8, G = COLS / W;
   constexpr int K = LN ? 2 * R : R;               // sums a thread takes part in
   constexpr bool kGammaRegs = COLS <= 16;         // else in shared memory, behind the ring
-  using Cols = Group<T, W, ALIGNED, FULL, (G > 2)>;
-  using Sums = Group<float, W, ALIGNED, FULL, false>;
+  using Cols = Group<T, W, ALIGNED, false, false>;
+  using Sums = Group<float, W, ALIGNED, false, false>;
   extern __shared__ __align__(128) uint8_t smem[];
   if (blockIdx.x >= static_cast<unsigned>(p.row_blocks)) {
     column_block<T, LN, ALIGNED>(p, reinterpret_cast<float*>(smem));
@@ -123,10 +126,23 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
   __shared__ __align__(8) uint64_t bars[kMostStages];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tpr = p.tpr, groups = blockDim.x / tpr;
+  const int tpr = SUB < 32 ? SUB : p.tpr;
   const int group = tid / tpr, t = tid - group * tpr;
-  const int warps = tpr >> 5, warp0 = group * warps;
+  const int warps = tpr >> 5, warp0 = group * warps;  // of a row; SUB < 32: none
   const int n = rp.n;
+  if constexpr (ALIGNED) {
+    const int rows = rp.stages * rp.rows * (RES ? 3 : 2), tail = static_cast<int>(rp.pitch - rp.row_bytes) / 16;
+    for (int i = tid; i < rows * tail; i += blockDim.x) {
+      const int r = i / tail;
+      *reinterpret_cast<uint4*>(smem + r * rp.pitch + rp.row_bytes + (i - r * tail) * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  const auto load = [&](float2 (&v)[W / 2], const T* row, int j) {
+    if constexpr (ALIGNED)
+      Cols::load_padded(v, row, t, tpr, j);
+    else
+      Cols::load(v, row, t, tpr, j, n);
+  };
   const int64_t row_step = static_cast<int64_t>(p.row_blocks) * rp.rows;
   int64_t block_row = static_cast<int64_t>(blockIdx.x) * rp.rows;
   RowRing<T, RES ? 3 : 2, ALIGNED> ring(rp, smem, bars, &abort_flag, block_row, row_step);
@@ -168,11 +184,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) dg[j][i] = db[j][i] = make_float2(0.0f, 0.0f);
   }
-  // The rows' statistics, fetched one row block ahead: lane r holds row r's
-  // rstd, lane R + r its mean; zeros for rows past the last.
-  const float* stat = LN && lane >= R ? p.mean : static_cast<const float*>(p.rstd);
-  const int stat_row = LN && lane >= R ? lane - R : lane;
-  const bool stat_lane = lane < K && !(p.rstd64 && lane < R);
+  // The rows' statistics, fetched one row block ahead: lane r (of SUB) holds
+  // row r's rstd, lane R + r its mean; zeros for rows past the last.
+  const int sub = lane % SUB, sub0 = lane - sub;
+  const float* stat = LN && sub >= R ? p.mean : static_cast<const float*>(p.rstd);
+  const int stat_row = LN && sub >= R ? sub - R : sub;
+  const bool stat_lane = sub < K && !(p.rstd64 && sub < R);
   float next = 0.0f;
   double next64 = 0.0;
   auto statistics = [&](int64_t row) {
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
     if (stat_lane && row + stat_row < rp.M) next = stat[row + stat_row];
     if (p.rstd64) {
       next64 = 0.0;
-      if (lane < R && row + lane < rp.M) next64 = static_cast<const double*>(p.rstd)[row + lane];
+      if (sub < R && row + sub < rp.M) next64 = static_cast<const double*>(p.rstd)[row + sub];
     }
   };
   statistics(block_row + group * R);
@@ -190,11 +207,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
     const int64_t row0 = block_row + group * R;
     float2 mean[R];  // negated
     float rstd[R];
-    if (p.rstd64 && lane < R) next = static_cast<float>(next64);
+    if (p.rstd64 && sub < R) next = static_cast<float>(next64);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      rstd[r] = __shfl_sync(0xffffffffu, next, r);
-      const float a = LN ? -__shfl_sync(0xffffffffu, next, R + r) : 0.0f;
+      rstd[r] = __shfl_sync(0xffffffffu, next, sub0 + r);
+      const float a = LN ? -__shfl_sync(0xffffffffu, next, sub0 + R + r) : 0.0f;
       mean[r] = make_float2(a, a);
     }
     statistics(row0 + row_step);
@@ -221,8 +238,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float2 x[W / 2], y[W / 2], gj[W / 2];
-        Cols::load(x, sx, t, tpr, j, n);
-        Cols::load(y, sy, t, tpr, j, n);
+        load(x, sx, j);
+        load(y, sy, j);
         if constexpr (!kGammaRegs) kept_gamma(gj, j);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
@@ -237,24 +254,34 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
       v[r] = s2.x + s2.y;
       if constexpr (LN) v[R + r] = s1.x + s1.y;
     }
-    int index;
-    const float part = warp_sums<K>(v, lane, index);
-    if ((lane & (32 / K - 1)) == 0) red[buf][warp][index] = part;
-    __syncthreads();  // the last use of red[buf] and of the previous stage is over
-    if (warp == 0 && begun) ring.fetch();
-    // lane w * K + k adds value k of every (32 / K)-th warp from w on
     float sum = 0.0f;
-    for (int w = lane / K; w < warps; w += 32 / K) sum += red[buf][warp0 + w][lane % K];
+    if constexpr (SUB < 32) {
+      sum = sub_sums<K, SUB>(v, lane);
+      __syncthreads();  // the last use of the previous stage is over
+      if (warp == 0 && begun) ring.fetch();
+    } else {
+      int index;
+      const float part = warp_sums<K>(v, lane, index);
+      if ((lane & (32 / K - 1)) == 0) red[buf][warp][index] = part;
+      __syncthreads();  // the last use of red[buf] and of the previous stage is over
+      if (warp == 0 && begun) ring.fetch();
+      // lane w * K + k adds value k of every (32 / K)-th warp from w on
+      for (int w = lane / K; w < warps; w += 32 / K) sum += red[buf][warp0 + w][lane % K];
 #pragma unroll
-    for (int o = K; o < 32; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = K; o < 32; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    const auto value = [&](int k) {
+      if constexpr (SUB < 32) return sub_sum_of<K, SUB>(sum, lane, k);
+      return __shfl_sync(0xffffffffu, sum, k % 32);
+    };
     sum *= -p.inv_n;
     // dx = rstd * g + (-rstd * c1) + (x - mean) * (-rstd^2 * c2)
     T* dx = static_cast<T*>(p.dx) + row0 * p.lddx;
 #pragma unroll
     for (int r = 0; r < R; ++r, dx += p.lddx) {
-      const float k2 = __shfl_sync(0xffffffffu, sum, r) * rstd[r] * rstd[r];
-      const float k1 = LN ? __shfl_sync(0xffffffffu, sum, (R + r) % 32) * rstd[r] : 0.0f;
-      if (r >= live) break;
+      const float k2 = value(r) * rstd[r] * rstd[r];
+      const float k1 = LN ? value(R + r) * rstd[r] : 0.0f;
+      if (SUB == 32 && r >= live) break;  // (SUB < 32: the warp's other rows may live)
       const float2 c1 = make_float2(k1, k1), c2 = make_float2(k2, k2), rs = make_float2(rstd[r], rstd[r]);
       const T* sx = ring.row(0, block_row, group * R + r);
       const T* sy = ring.row(1, block_row, group * R + r);
@@ -262,9 +289,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float2 x[W / 2], y[W / 2], z[W / 2], gj[W / 2];
-        Cols::load(x, sx, t, tpr, j, n);
-        Cols::load(y, sy, t, tpr, j, n);
-        if (RES) Cols::load(z, sr, t, tpr, j, n);
+        load(x, sx, j);
+        load(y, sy, j);
+        if (RES) load(z, sr, j);
         if constexpr (!kGammaRegs) kept_gamma(gj, j);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
@@ -273,18 +300,34 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
           d = __ffma2_rn(g, rs, d);
           x[i] = RES ? __fadd2_rn(d, z[i]) : d;
         }
-        Cols::store(dx, x, t, tpr, j, n);
+        if (SUB == 32 || r < live) Cols::store(dx, x, t, tpr, j, n);
       }
     }
     ring.next();
   }
   if (ring.finish(tid == 0) || p.partial == nullptr) return;
-  // the block's groups in order, through the ring's memory (no copy is in
-  // flight any more), then one row of sums
+  // A warp's rows, then the block's groups (SUB < 32: its warps) in order,
+  // through the ring's memory (no copy is in flight any more), then one row of
+  // sums.
+  if constexpr (SUB < 32) {
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i)
+#pragma unroll
+        for (int o = SUB; o < 32; o *= 2) {
+          dg[j][i].x += __shfl_xor_sync(0xffffffffu, dg[j][i].x, o);
+          dg[j][i].y += __shfl_xor_sync(0xffffffffu, dg[j][i].y, o);
+          if (LN) db[j][i].x += __shfl_xor_sync(0xffffffffu, db[j][i].x, o);
+          if (LN) db[j][i].y += __shfl_xor_sync(0xffffffffu, db[j][i].y, o);
+        }
+  }
+  const int joins = SUB < 32 ? blockDim.x / 32 : blockDim.x / tpr, mine = SUB < 32 ? warp : group;
+  const bool holds = SUB == 32 || lane < SUB;
   float* join = reinterpret_cast<float*>(smem);  // [LN ? 2 : 1][N]
-  for (int k = 1; k < groups; ++k) {
+  for (int k = 1; k < joins; ++k) {
     __syncthreads();
-    if (group == k) {
+    if (mine == k && holds) {
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         Sums::store(join, dg[j], t, tpr, j, n);
@@ -292,7 +335,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
       }
     }
     __syncthreads();
-    if (group == 0) {
+    if (mine == 0 && holds) {
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float2 a[W / 2], b[W / 2];
@@ -306,7 +349,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
       }
     }
   }
-  if (group == 0) {
+  if (mine == 0 && holds) {
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * (LN ? 2 : 1) * n;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -399,15 +442,60 @@ __global__ void __launch_bounds__(512) norm_param_grad_kernel(const float* __res
 // Shared memory for gamma.
 int64_t gamma_bytes(const RowPlan& b, int64_t size) { return b.cols > 16 ? static_cast<int64_t>(b.tpr) * b.cols * size : 0; }
 
-// As many rows between two barriers as leave the ring two stages (measured at
-// [16384, 2048] BF16 with a residual, LayerNorm, 8 columns a thread: 75 us with
-// one row, 57 with two, 51 with four).
+// Rows of up to 128 columns: 8 lanes each.  Else the fewest threads and
+// columns a thread that hold the row, 512 threads an SM, and as many rows
+// between two barriers as leave the ring two stages (measured at [16384, 2048]
+// BF16 with a residual, LayerNorm, 8 columns a thread: 75 us with one row, 57
+// with two, 51 with four).
 RowPlan plan_bwd(int64_t M, int64_t N, int64_t size, int tensors, bool aligned, bool packed, bool wide_gamma, int sms) {
-  const int least = aligned ? static_cast<int>(16 / size) : 8;
-  const RowChoice choices[] = {{256, least, 4}, {256, 8, 4}, {256, 16, 2}, {512, 16, 2}, {512, 32, 1}};
   if (aligned && (N * size) % 16 != 0) return RowPlan{};
-  return plan_rows(choices, 5, M, N, size, tensors, aligned, packed, sms, [](int threads, int) { return threads > 256 ? 1 : 2; },
-                   [&](const RowPlan& b) { return gamma_bytes(b, wide_gamma ? 4 : size); });
+  struct Choice {
+    int threads, cols, rows;
+  };
+  const int least = aligned ? static_cast<int>(16 / size) : 8;
+  const Choice choices[] = {{256, least, 4}, {256, 8, 4}, {256, 16, 2}, {512, 16, 2}, {512, 32, 1}};
+  RowPlan b{};
+  if (N <= 128) {
+    b.tpr = 8;
+    b.cols = N <= 64 ? 8 : 16;
+    b.rows = 2;
+    b.groups = 256 / b.tpr;
+  }
+  for (const Choice& c : choices) {
+    if (b.cols != 0) break;
+    const int64_t tpr = ((N + c.cols - 1) / c.cols + 31) / 32 * 32;
+    if (tpr > c.threads) continue;
+    b.cols = c.cols;
+    b.tpr = static_cast<int>(tpr);
+    b.rows = c.rows;
+    b.groups = 1;
+    for (int g = 2; g * b.tpr <= 256; ++g)  // the groups that leave the fewest of 512 threads out
+      if (512 / (g * b.tpr) * g >= 512 / (b.groups * b.tpr) * b.groups) b.groups = g;
+  }
+  if (b.cols == 0) return b;
+  const int per_sm = 512 / (b.tpr * b.groups);
+  const int64_t row = N * size;
+  const int64_t pitch = aligned ? static_cast<int64_t>(b.tpr) * b.cols * size : packed ? row : (row + 30) / 16 * 16;
+  const int64_t room = kRingBytes / per_sm - kRingExtra - gamma_bytes(b, wide_gamma ? 4 : size);
+  const auto stage = [&](int rows) {
+    const int64_t bytes = pitch * b.groups * rows;
+    return (aligned ? bytes : (bytes + 30) / 16 * 16) * tensors;
+  };
+  while (b.rows > 1 && room / stage(b.rows) < 2) b.rows /= 2;
+  const int64_t stages = std::min<int64_t>(kMostStages, room / stage(b.rows));
+  if (stages < 2) return RowPlan{};
+  const int64_t rows = static_cast<int64_t>(b.groups) * b.rows;
+  b.blocks = std::min<int64_t>((M + rows - 1) / rows, static_cast<int64_t>(per_sm) * sms);
+  b.ring.M = M;
+  b.ring.n = static_cast<int>(N);
+  b.ring.rows = static_cast<int>(rows);
+  b.ring.stages = static_cast<int>(stages);
+  b.ring.row_bytes = static_cast<uint32_t>(row);
+  b.ring.pitch = static_cast<uint32_t>(pitch);
+  b.ring.stage_bytes = static_cast<uint32_t>(stage(b.rows));
+  b.ring.tensor_bytes = b.ring.stage_bytes / static_cast<uint32_t>(tensors);
+  b.ring.packed = packed && pitch == row;
+  return b;
 }
 
 // Rows too long for a block: the blocks that share each column's sum.
@@ -420,14 +508,15 @@ int64_t long_blocks(int64_t M, int64_t N, int sms) {
 // column blocks run beside the others.)
 bool small_batch(int64_t M, int64_t N) { return M <= 1024 && M * N <= int64_t{1} << 22; }
 
-template <class T, int COLS, int R, bool LN, bool RES, bool ALIGNED, bool FULL>
+template <class T, int COLS, int R, int SUB, bool LN, bool RES, bool ALIGNED>
 cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
+  if (b.cols != COLS || b.rows != R || (SUB < 32 && b.tpr != SUB)) return cudaErrorInvalidValue;  // a plan without a kernel
   p.tpr = b.tpr;
   p.row_blocks = static_cast<int>(b.blocks);
   const int64_t slice = ALIGNED ? 128 / static_cast<int64_t>(sizeof(T)) : 32;
   const bool columns = p.dgamma != nullptr || p.dbeta != nullptr;
   const int64_t slices = columns ? (p.N + slice - 1) / slice : 0;
-  const auto kern = norm_bwd_kernel<T, COLS, R, LN, RES, ALIGNED, FULL>;
+  const auto kern = norm_bwd_kernel<T, COLS, R, SUB, LN, RES, ALIGNED>;
   const int64_t smem = std::max<int64_t>(static_cast<int64_t>(b.ring.stage_bytes) * b.ring.stages +
                                              gamma_bytes(b, p.p32 || p.gamma == nullptr ? 4 : sizeof(T)),
                                          std::max<int64_t>(b.groups > 1 ? p.N * (LN ? 8 : 4) : 0,
@@ -445,33 +534,24 @@ cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <class T, int COLS, int R, bool LN, bool ALIGNED>
-cudaError_t run_rows(const BwdParams& p, const RowPlan& b, cudaStream_t stream) {
-  if constexpr (ALIGNED)
-    if (p.N == static_cast<int64_t>(b.tpr) * COLS)
-      return p.dres != nullptr ? run_as<T, COLS, R, LN, true, true, true>(p, b, stream)
-                               : run_as<T, COLS, R, LN, false, true, true>(p, b, stream);
-  return p.dres != nullptr ? run_as<T, COLS, R, LN, true, ALIGNED, false>(p, b, stream)
-                           : run_as<T, COLS, R, LN, false, ALIGNED, false>(p, b, stream);
-}
-
-template <class T, int COLS, bool LN, bool ALIGNED>
+template <class T, int COLS, int R, int SUB, bool LN, bool ALIGNED>
 cudaError_t run(const BwdParams& p, const RowPlan& b, cudaStream_t stream) {
-  if constexpr (COLS <= 8)
-    if (b.rows == 4) return run_rows<T, COLS, 4, LN, ALIGNED>(p, b, stream);
-  if constexpr (COLS <= 16)
-    if (b.rows == 2) return run_rows<T, COLS, 2, LN, ALIGNED>(p, b, stream);
-  return run_rows<T, COLS, 1, LN, ALIGNED>(p, b, stream);
+  return p.dres != nullptr ? run_as<T, COLS, R, SUB, LN, true, ALIGNED>(p, b, stream)
+                           : run_as<T, COLS, R, SUB, LN, false, ALIGNED>(p, b, stream);
 }
 
 template <class T, bool LN, bool ALIGNED>
 cudaError_t run_plan(const BwdParams& p, const RowPlan& b, cudaStream_t stream) {
+  if (b.tpr == 8) {
+    if (b.cols == 8) return run<T, 8, 2, 8, LN, ALIGNED>(p, b, stream);
+    return b.rows == 2 ? run<T, 16, 2, 8, LN, ALIGNED>(p, b, stream) : run<T, 16, 1, 8, LN, ALIGNED>(p, b, stream);
+  }
   if constexpr (ALIGNED && sizeof(T) == 4)
-    if (b.cols == 4) return run<T, 4, LN, ALIGNED>(p, b, stream);
+    if (b.cols == 4) return run<T, 4, 4, 32, LN, ALIGNED>(p, b, stream);
   switch (b.cols) {
-    case 8: return run<T, 8, LN, ALIGNED>(p, b, stream);
-    case 16: return run<T, 16, LN, ALIGNED>(p, b, stream);
-    default: return run<T, 32, LN, ALIGNED>(p, b, stream);
+    case 8: return b.rows == 4 ? run<T, 8, 4, 32, LN, ALIGNED>(p, b, stream) : run<T, 8, 2, 32, LN, ALIGNED>(p, b, stream);
+    case 16: return b.rows == 2 ? run<T, 16, 2, 32, LN, ALIGNED>(p, b, stream) : run<T, 16, 1, 32, LN, ALIGNED>(p, b, stream);
+    default: return run<T, 32, 1, 32, LN, ALIGNED>(p, b, stream);
   }
 }
 

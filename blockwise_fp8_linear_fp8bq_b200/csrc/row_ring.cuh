@@ -179,6 +179,14 @@ struct Group {
     return ALIGNED ? (t + j * stride) * W + k : t + (j * W + k) * stride;
   }
 
+  // The same from a row padded with zeros to every thread's columns.
+  __device__ static __forceinline__ void load_padded(float2 (&v)[W / 2], const T* row, int t, int stride, int j) {
+    Pack<T, W> x;
+    load_pack(x, row + column(t, stride, j, 0));
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) v[i] = x.f2(i);
+  }
+
   // Whether every thread's j-th group lies within the row.
   __device__ static __forceinline__ bool whole(int stride, int j, int n) { return FULL || (SPLIT && (j + 1) * W * stride <= n); }
 
@@ -292,6 +300,29 @@ __device__ __forceinline__ float warp_sum_of(float s, int k) {
   return __shfl_sync(0xffffffffu, s, k * (32 / K));
 }
 
+// The same within each SUB lanes.
+template <int K, int SUB>
+__device__ __forceinline__ float sub_sums(float (&v)[K], int lane) {
+  int o = SUB / 2;
+#pragma unroll
+  for (int k = K; k > 1; k /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < k / 2; ++i) {
+      const float give = upper ? v[i] : v[i + k / 2], keep = upper ? v[i + k / 2] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (; o >= 1; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+template <int K, int SUB>
+__device__ __forceinline__ float sub_sum_of(float s, int lane, int k) {
+  return __shfl_sync(0xffffffffu, s, (lane & ~(SUB - 1)) + k * (SUB / K));
+}
+
 // Sums of two values over the block (every thread gets them), through
 // red[warps].  The caller separates uses of one `red` by a barrier.
 __device__ __forceinline__ float2 block_sum2(float2 v, float2* red) {
@@ -317,53 +348,5 @@ struct RowPlan {
   int64_t blocks;
   RingParams ring;
 };
-
-struct RowChoice {
-  int threads, cols, rows;  // at most so many threads a row; columns a thread; rows between barriers, halved to fit
-};
-
-// The first choice that holds a row of N columns; `width` columns a group.
-// per_sm(threads, cols) blocks run on an SM, and extra(plan) is what a block
-// needs of shared memory beside its ring.
-template <class F, class E>
-inline RowPlan plan_rows(const RowChoice* choices, int count, int64_t M, int64_t N, int64_t size, int tensors, bool aligned,
-                         bool packed, int sms, F per_sm, E extra) {
-  RowPlan b{};
-  for (int i = 0; i < count && b.cols == 0; ++i) {
-    const RowChoice& c = choices[i];
-    const int64_t tpr = ((N + c.cols - 1) / c.cols + 31) / 32 * 32;
-    if (tpr > c.threads) continue;
-    b.cols = c.cols;
-    b.tpr = static_cast<int>(tpr);
-    b.rows = c.rows;
-  }
-  if (b.cols == 0) return b;
-  b.groups = std::max(1, 256 / b.tpr);
-  const int on_sm = per_sm(b.tpr * b.groups, b.cols);
-  const int64_t room = kRingBytes / on_sm - kRingExtra - extra(b), row = N * size;
-  const int64_t pitch = aligned || packed ? row : (row + 30) / 16 * 16;
-  const auto stage = [&](int rows) {
-    const int64_t bytes = pitch * b.groups * rows;
-    return (aligned ? bytes : (bytes + 30) / 16 * 16) * tensors;
-  };
-  while (b.rows > 1 && room / stage(b.rows) < 2) b.rows /= 2;
-  const int64_t stages = std::min<int64_t>(kMostStages, room / stage(b.rows));
-  if (stages < 2) {
-    b.cols = 0;
-    return b;
-  }
-  const int64_t rows = static_cast<int64_t>(b.groups) * b.rows;
-  b.blocks = std::min<int64_t>((M + rows - 1) / rows, static_cast<int64_t>(on_sm) * sms);
-  b.ring.M = M;
-  b.ring.n = static_cast<int>(N);
-  b.ring.rows = static_cast<int>(rows);
-  b.ring.stages = static_cast<int>(stages);
-  b.ring.row_bytes = static_cast<uint32_t>(row);
-  b.ring.pitch = static_cast<uint32_t>(pitch);
-  b.ring.stage_bytes = static_cast<uint32_t>(stage(b.rows));
-  b.ring.tensor_bytes = b.ring.stage_bytes / static_cast<uint32_t>(tensors);
-  b.ring.packed = packed;
-  return b;
-}
 
 }  // namespace fp8bq

@@ -13,7 +13,10 @@ pytestmark = pytest.mark.gpu
 DTYPES = [torch.bfloat16, torch.float16, torch.float32]
 # (rows, columns, extra leading dimension)
 SIZES = [(1, 1, 0), (3, 7, 0), (5, 64, 8), (1, 640, 0), (200, 1283, 0), (130, 1280, 3), (509, 2048, 0), (33, 4100, 0),
-         (300, 4096, 16), (40, 6144, 0), (7, 8192, 0), (3, 8200, 0), (5, 16384, 0), (3, 20001, 0), (2, 70000, 0)]
+         (300, 4096, 16), (40, 6144, 0), (7, 8192, 0), (3, 8200, 0), (5, 16384, 0), (3, 20001, 0), (2, 70000, 0),
+         (2000, 64, 0), (2001, 128, 8), (3000, 77, 0), (1500, 120, 1), (1100, 256, 0), (1027, 250, 0), (1025, 320, 0),
+         (1200, 1000, 24), (1100, 1048, 0), (1030, 2047, 0), (1030, 2100, 0), (1026, 5000, 0), (1025, 12288, 0),
+         (600, 12287, 0), (300, 14000, 0)]
 
 
 def draw(gen, rows, cols, dtype, ld=0, std=1.0, mean=0.0):
