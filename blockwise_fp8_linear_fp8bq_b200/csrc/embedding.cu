@@ -101,6 +101,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kSortCluster = 8;
+constexpr int kKept = 4;  // rounds of 32 tokens a warp keeps in registers: all, up to 32768 tokens
 
 // A sorted token: its id (V: none of the table's rows) and its position.
 struct alignas(8) Token {
@@ -161,12 +162,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
     };
     for (int b = lane; b < bins; b += 32) mine[b] = 0;
     __syncwarp();
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-      const bool live = i0 + lane < end;
-      const uint32_t d = live ? (read(i0 + lane).id >> shift) & (bins - 1) : bins;
+    // the warp's first tokens stay in registers for the second walk
+    Token kept[kKept];
+#pragma unroll
+    for (int j = 0; j < kKept; ++j)
+      if (begin + j * 32 + lane < end) kept[j] = read(begin + j * 32 + lane);
+    const auto count_one = [&](bool live, Token k) {
+      const uint32_t d = live ? (k.id >> shift) & (bins - 1) : bins;
       const uint32_t same = __match_any_sync(0xffffffffu, d);
       if (live && lane == __ffs(same) - 1) mine[d] += __popc(same);
       __syncwarp();
+    };
+#pragma unroll
+    for (int j = 0; j < kKept; ++j)
+      if (begin + j * 32 < end) count_one(begin + j * 32 + lane < end, kept[j]);
+    for (int64_t i0 = begin + kKept * 32; i0 < end; i0 += 32) {
+      const bool live = i0 + lane < end;
+      count_one(live, live ? read(i0 + lane) : Token{});
     }
     __syncthreads();
     // per digit: where each warp's tokens start within the block's
@@ -209,10 +221,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
       base[tid] = lower + incl - all + before;
     }
     __syncthreads();
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-      const bool live = i0 + lane < end;
-      Token k{};
-      if (live) k = read(i0 + lane);
+    const auto place_one = [&](bool live, Token k) {
       const uint32_t d = live ? (k.id >> shift) & (bins - 1) : bins;
       const uint32_t same = __match_any_sync(0xffffffffu, d);
       uint32_t at = 0;
@@ -221,6 +230,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
       if (live && lane == __ffs(same) - 1) mine[d] += __popc(same);
       __syncwarp();
       if (live) __stcg(reinterpret_cast<uint2*>(to + at), make_uint2(k.id, k.pos));
+    };
+#pragma unroll
+    for (int j = 0; j < kKept; ++j)
+      if (begin + j * 32 < end) place_one(begin + j * 32 + lane < end, kept[j]);
+    for (int64_t i0 = begin + kKept * 32; i0 < end; i0 += 32) {
+      const bool live = i0 + lane < end;
+      place_one(live, live ? read(i0 + lane) : Token{});
     }
     // the next pass reads what the whole cluster wrote, and rewrites `total`
     if (p.sorters > 1)
@@ -295,13 +311,14 @@ __global__ void __launch_bounds__(256) grad_chunk_kernel(const GradParams p) {
   constexpr int kBatch = 8;
   cudaGridDependencySynchronize();
   const int tx = threadIdx.x & (p.cols - 1), ty = threadIdx.x / p.cols;
-  const int64_t chunk = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.cols) + ty;
-  const int c = (blockIdx.y * p.cols + tx) * VEC;
+  const int64_t chunk = static_cast<int64_t>(blockIdx.y) * (blockDim.x / p.cols) + ty;
+  const int c = (blockIdx.x * p.cols + tx) * VEC;
   if (chunk >= p.chunks || c >= p.D) return;
   const int64_t begin = chunk * p.chunk, end = min(begin + p.chunk, p.T);
   const uint32_t none = static_cast<uint32_t>(p.V);
   uint32_t cur = p.tokens[begin].id;
   bool head = begin > 0 && p.tokens[begin - 1].id == cur;
+  const T* dy = static_cast<const T*>(p.dy) + c;
   float acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(256) grad_chunk_kernel(const GradParams p) {
     for (int k = 0; k < kBatch; ++k) tok[k] = i0 + k < end ? p.tokens[i0 + k] : Token{none, 0};
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (tok[k].id != none) load_pack<true>(v[k], static_cast<const T*>(p.dy) + tok[k].pos * p.lddy + c);
+      if (tok[k].id != none) load_pack<true>(v[k], dy + tok[k].pos * p.lddy);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (i0 + k >= end) break;
@@ -370,12 +387,18 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p) {
     load_pack(v, src + (chunk * 2 + 1) * static_cast<int64_t>(p.D));
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = v.v[i];
-#pragma unroll 4
-    for (int64_t k = chunk + 1; k <= last; ++k) {
-      Pack<float, VEC> u;
-      load_pack(u, src + k * 2 * static_cast<int64_t>(p.D));
+    constexpr int kBatch = VEC == 8 ? 8 : 16;
+    for (int64_t k0 = chunk + 1; k0 <= last; k0 += kBatch) {
+      Pack<float, VEC> u[kBatch];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += u.v[i];
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k <= last) load_pack(u[k], src + (k0 + k) * 2 * static_cast<int64_t>(p.D));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k <= last) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] += u[k].v[i];
+        }
     }
     write_row<G, VEC>(p, cur, c, acc);
   }
@@ -472,7 +495,7 @@ __global__ void __launch_bounds__(256) grad_few_kernel(const FewParams p) {
   }
 }
 
-bool few_tokens(int64_t T, int64_t V, int64_t D) { return T > 0 && T <= kFewTokens && V * D * 4 <= kFewBytes; }
+bool few_tokens(int64_t T, int64_t V, int64_t D) { return T > 0 && T <= kFewTokens && V * D <= kFewBytes / 4; }
 
 // Tokens a chunk: few enough that short batches fill the GPU, and at most
 // about a thousand chunks, whose partial sums are the workspace.
@@ -490,8 +513,8 @@ cudaError_t run_grad(GradParams p, cudaStream_t stream) {
   p.cols = 1;
   while (p.cols < slots && p.cols < 256) p.cols *= 2;
   const int rows = 256 / p.cols;
-  const dim3 grid(static_cast<unsigned>((p.chunks + rows - 1) / rows),
-                  static_cast<unsigned>((slots + p.cols - 1) / p.cols));
+  // the pieces of a row next to each other, so that they are read together
+  const dim3 grid(static_cast<unsigned>((slots + p.cols - 1) / p.cols), static_cast<unsigned>((p.chunks + rows - 1) / rows));
   cudaError_t e = launch_dependent(grad_chunk_kernel<T, G, VEC>, grid, dim3(256), 0, stream, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
   const int threads = std::min(256, (slots + 31) / 32 * 32);
@@ -504,7 +527,14 @@ cudaError_t grad_of_type(const FewParams& f, bool few, cudaStream_t stream) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
   const GradParams& p = f.g;
   const bool wide = p.D % kVec == 0 && rows_aligned(p.dy, p.lddy, sizeof(T), 16) && rows_aligned(p.dw, p.lddw, sizeof(G), 16);
-  if (!few) return wide ? run_grad<T, G, kVec>(p, stream) : run_grad<T, G, 1>(p, stream);
+  const bool pairs = sizeof(T) == 2 && p.D % 2 == 0 && rows_aligned(p.dy, p.lddy, sizeof(T), 4) &&
+                     rows_aligned(p.dw, p.lddw, sizeof(G), 2 * sizeof(G));
+  if (!few) {
+    if (wide) return run_grad<T, G, kVec>(p, stream);
+    if constexpr (sizeof(T) == 2)
+      if (pairs) return run_grad<T, G, 2>(p, stream);
+    return run_grad<T, G, 1>(p, stream);
+  }
   const int64_t zeros = p.accumulate ? 0 : (f.z.V + f.z.rows - 1) / f.z.rows;
   const unsigned blocks = static_cast<unsigned>(p.T + zeros);
   if (wide)

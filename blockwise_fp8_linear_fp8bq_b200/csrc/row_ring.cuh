@@ -114,6 +114,7 @@ struct RowRing {
         for (int k = 0; k < head; ++k) dst[k] = src[k];
         const int tail = to < e ? static_cast<int>((max(to, a) - a) / sizeof(T)) : count;
         for (int k = max(tail, head); k < count; ++k) dst[k] = src[k];
+        if (head > 0 || tail < count) fence_proxy_async_smem();  // a later copy may write these bytes
       }
       total = __reduce_add_sync(0xffffffffu, total);
       if (lane == 0) mbar_arrive_expect_tx(bar, total);

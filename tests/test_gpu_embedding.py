@@ -125,6 +125,29 @@ def test_gradient_full_size():
     assert not dw.any()
 
 
+@pytest.mark.parametrize("by", [1, 2, 5])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V,D", [(50, 11, 30), (1500, 300, 64), (5000, 40, 129)])
+def test_rows_that_start_anywhere(T, V, D, dtype, by):
+    """Tables, rows and gradients whose first value is at no multiple of 16 bytes."""
+    gen = gen_of(T + by)
+    place = lambda n: torch.full((n + 20,), float("nan"), dtype=dtype, device="cuda")
+    w = place(V * D)[by:by + V * D].view(V, D)
+    w.copy_(torch.randn(V, D, generator=gen, device="cuda"))
+    dy = place(T * D)[by + 1:by + 1 + T * D].view(T, D)
+    dy.copy_(torch.randn(T, D, generator=gen, device="cuda") * 0.01)
+    ids = ids_of(gen, T, V, "text")
+    ybuf = torch.full((T * D + 20,), 7.0, dtype=dtype, device="cuda")
+    y = fp.embedding_forward(w, ids, out=ybuf[by:by + T * D].view(T, D))
+    assert torch.equal(y, w[ids]) and (ybuf[:by] == 7.0).all() and (ybuf[by + T * D:] == 7.0).all()
+    for grad in {dtype, torch.float32}:
+        buf = torch.full((V * D + 20,), 7.0, dtype=grad, device="cuda")
+        dw = fp.embedding_backward(dy, ids, V, out=buf[by:by + V * D].view(V, D))
+        ref, bound = embedding_backward(dy, ids, V, 1.0, None)
+        assert_within(dw, ref, bound + half_ulp(grad) * (ref.abs() + bound), "dw")
+        assert (buf[:by] == 7.0).all() and (buf[by + V * D:] == 7.0).all()
+
+
 def test_gradient_of_no_tokens():
     ids = torch.empty(0, dtype=torch.int64, device="cuda")
     dy = torch.empty(0, 64, device="cuda")

@@ -64,6 +64,65 @@ def test_layernorm_forward(M, N, pad, dtype, mode):
     assert torch.equal(y2, y)
 
 
+def shifted(t, by, fill=float("nan")):
+    """t's values `by` elements into a buffer: rows that start anywhere."""
+    flat = torch.full((t.numel() + by + 9,), fill, dtype=t.dtype, device="cuda")
+    view = flat[by:by + t.numel()].view(t.shape)
+    view.copy_(t)
+    return flat, view
+
+
+@pytest.mark.parametrize("by", [1, 3, 4, 7])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", [(1, 1), (2, 3), (5, 64), (2100, 64), (70, 333), (400, 640), (3, 5000), (1, 9)])
+def test_rows_that_start_anywhere(M, N, dtype, by):
+    """Tensors whose first value is at no multiple of 16 bytes, in a buffer of
+    NaN, every one of them at another offset."""
+    gen = gen_of(M + N + by)
+    _, x = shifted(draw(gen, M, N, dtype, mean=0.5), by)
+    _, dy = shifted(draw(gen, M, N, dtype, std=0.01), by + 1)
+    _, dres = shifted(draw(gen, M, N, dtype, std=0.01), by + 2)
+    gamma, beta = params(gen, N, dtype, "same")
+    _, gamma = shifted(gamma, by)
+    ybuf, y = shifted(torch.zeros_like(x), by + 3, 7.0)
+    got, mean, rstd = fp.layernorm_forward(x, gamma, beta, 1e-5, out=(y, None, None))
+    ry, _, _, bound = layernorm(x, gamma, beta, 1e-5)
+    assert_within(got, ry, bound + half_ulp(dtype) * (ry.abs() + bound), "y")
+    assert (ybuf[:by + 3] == 7.0).all() and (ybuf[by + 3 + M * N:] == 7.0).all()
+    for kind in ("ln", "rms"):
+        mean, rstd = statistics(x, kind)
+        dbuf, dx = shifted(torch.zeros_like(x), by, 7.0)
+        out = (dx, None, None) if kind == "ln" else (dx, None)
+        check_backward(kind, dy, x, mean, rstd, gamma, dres, run_backward(kind, dy, x, mean, rstd, gamma, dres, out=out))
+        assert (dbuf[:by] == 7.0).all() and (dbuf[by + M * N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N", [(40, 2048), (1500, 2048), (1500, 77)])
+def test_two_backward_passes_at_once(M, N):
+    """On two streams at the same time, each with its own workspace, and dx
+    written over x as well as over dy."""
+    gen = gen_of(21)
+    x, dy = draw(gen, M, N, torch.bfloat16), draw(gen, M, N, torch.bfloat16, std=0.01)
+    gamma, _ = params(gen, N, torch.bfloat16, "same")
+    mean, rstd = statistics(x, "ln")
+    want = fp.layernorm_backward(dy, x, mean, rstd, gamma)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(fp.layernorm_backward(dy, x, mean, rstd, gamma))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    over = x.clone()
+    got = fp.layernorm_backward(dy, over, mean, rstd, gamma, out=(over, None, None))
+    assert torch.equal(got[0], want[0])
+    check_backward("ln", dy, x, mean, rstd, gamma, None, got)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_layernorm_forward_far_from_zero(dtype):
     """Rows whose mean is far larger than their spread, constant rows and a
