@@ -15,7 +15,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -540,92 +539,21 @@ def linear_wgrad(dy: torch.Tensor, x: torch.Tensor, fmt: int = SCALE_FP32) -> to
     return gemm(row_operand(qdt, sdt, fmt), row_operand(qxt, sxt, fmt))
 
 
-_ROW_DTYPES = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
-_ID_DTYPES = {torch.int32: 0, torch.int64: 1}
-_F32 = torch.float32
+_rows = None
 
 
-def _rows(t: torch.Tensor, name: str):
-    """Checks a 2-D row-major bf16, fp16 or fp32 CUDA tensor: (dtype code, leading dimension)."""
-    code = _ROW_DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be bf16, fp16 or fp32")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be a 2-D row-major tensor")
-    ld, inner = t.stride()
-    rows, cols = shape
-    if inner != 1 and cols > 1:
-        raise ValueError(f"{name} must be a 2-D row-major tensor")
-    if not t.is_cuda:
-        raise ValueError("fp8bq runs on CUDA tensors only (no CPU path)")
-    return code, ld if rows > 1 or ld >= cols else cols
-
-
-def _rows_like(t: torch.Tensor, name: str, x: torch.Tensor) -> int:
-    """The leading dimension of a tensor of x's shape, dtype and device."""
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
-        raise ValueError(f"{name} must be a {x.dtype} tensor of shape {tuple(x.shape)} on {x.device}")
-    return _rows(t, name)[1]
-
-
-def _new_rows(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
-
-
-def _vector(t: torch.Tensor, name: str, n: int, dtypes, device: int) -> int:
-    """Checks a contiguous vector of n entries and gives its address."""
-    if t.dtype not in dtypes or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} entries ({', '.join(map(str, dtypes))}) on device {device}")
-    return t.data_ptr()
-
-
-def _given(t: Optional[torch.Tensor], name: str, n: int, x: torch.Tensor, device: int):
-    """An fp32 vector of n entries to write, a new one for None, and its address."""
-    if t is None:
-        t = x.new_empty(n, dtype=_F32)
-        return t, t.data_ptr()
-    return t, _vector(t, name, n, (_F32,), device)
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() without its Stream object
-
-
-def _run(device: int, what: str, *args) -> None:
-    """Calls the library with `device` current, on its current stream."""
-    stream = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
-    f = getattr(_lib or lib(), what)
-    if torch.cuda.current_device() == device:
-        status = f(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            status = f(*args, stream)
-    if status != 0:
-        _raise(status, what)
-
-
-def _workspace(device: int, like: torch.Tensor, what: str, *args):
-    """A workspace of the size that `what` gives with `device` current: (tensor or None for
-    none, its address, its bytes)."""
-    f = getattr(_lib or lib(), what)
-    if torch.cuda.current_device() == device:
-        n = f(*args)
-    else:
-        with torch.cuda.device(device):
-            n = f(*args)
-    if n < 0:
-        raise RuntimeError(f"{what}: bad arguments or no usable device")
-    if n == 0:
-        return None, None, 0
-    ws = like.new_empty(n, dtype=torch.uint8)
-    return ws, ws.data_ptr(), n
-
-
-def _ids(ids: torch.Tensor, device: int) -> int:
-    wide = _ID_DTYPES.get(ids.dtype)
-    if wide is None or ids.get_device() != device or not ids.is_contiguous():
-        raise ValueError(f"ids must be a contiguous int32 or int64 tensor on device {device}")
-    return wide
+def _row_ops():
+    """The compiled binding of the row operators (raises if it has not been built)."""
+    global _rows
+    if _rows is None:
+        lib()
+        try:
+            from . import _row_binding
+        except ImportError as e:
+            raise ImportError(f"{e}; build it with `python -m blockwise_fp8_linear_fp8bq_b200.build`") from e
+        _row_binding.load(_LIB_PATH)
+        _rows = _row_binding
+    return _rows
 
 
 def embedding_forward(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
@@ -633,24 +561,7 @@ def embedding_forward(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, ou
     """scale * w[ids]: w [V, D] bf16, fp16 or fp32, ids int32 or int64 of any shape ->
     [*ids.shape, D] in `dtype` (w's by default), or `out`, a row-major [ids.numel(), D].
     An id outside [0, V) gives zeros and makes the next check() raise."""
-    code, ldw = _rows(w, "w")
-    V, D = w.shape
-    device = w.get_device()
-    wide, T = _ids(ids, device), ids.numel()
-    if out is None:
-        y = w.new_empty((*ids.shape, D), dtype=dtype)
-        ycode, ldy = code if dtype is None else _ROW_DTYPES.get(dtype, 0), D
-    else:
-        y = out
-        ycode, ldy = _rows(y, "out")
-        if y.shape != (T, D) or y.get_device() != device or (dtype is not None and y.dtype != dtype):
-            raise ValueError(f"out must have shape {(T, D)}, the dtype asked for and w's device")
-    _run(device, "fp8bq_embedding_forward", w.data_ptr(), V, D, ldw, ids.data_ptr(), wide, T, scale, y.data_ptr(), ldy,
-         code, ycode)
-    return y
-
-
-EMBEDDING_ACCUMULATE = 1
+    return (_rows or _row_ops()).embedding_forward(w, ids, scale, out, dtype)
 
 
 def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
@@ -661,31 +572,8 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: f
     dy is [*ids.shape, D] or [ids.numel(), D].  With accumulate=True the sums are added
     into `out`.  Tokens with id padding_id add nothing; an id outside [0, vocab) adds
     nothing and makes the next check() raise."""
-    T = ids.numel()
-    D = dy.shape[-1] if dy.dim() > 0 else 0
-    if dy.dim() != 2:
-        if dy.shape != (*ids.shape, D) or not dy.is_contiguous():
-            raise ValueError("dy must be [ids.numel(), D], or contiguous [*ids.shape, D]")
-        dy = dy.view(T, D)
-    code, lddy = _rows(dy, "dy")
-    if dy.shape[0] != T:
-        raise ValueError("dy must have a row for each id")
-    device = dy.get_device()
-    wide = _ids(ids, device)
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate=True needs the tensor to add into")
-        out = dy.new_empty((vocab, D), dtype=dtype)
-        wcode, lddw = _ROW_DTYPES.get(dtype, 0), D
-    else:
-        wcode, lddw = _rows(out, "out")
-        if out.shape != (vocab, D) or out.get_device() != device:
-            raise ValueError(f"out must have shape {(vocab, D)} and dy's device")
-    ws, pw, n = _workspace(device, dy, "fp8bq_embedding_workspace_bytes", T, D, vocab)
-    _run(device, "fp8bq_embedding_backward", dy.data_ptr(), T, D, lddy, ids.data_ptr(), wide, vocab, scale,
-         -1 if padding_id is None else padding_id, out.data_ptr(), lddw, code, wcode,
-         EMBEDDING_ACCUMULATE if accumulate else 0, pw, n)
-    return out
+    return (_rows or _row_ops()).embedding_backward(dy, ids, vocab, scale, -1 if padding_id is None else padding_id, out,
+                                                    accumulate, dtype)
 
 
 def layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
@@ -693,58 +581,8 @@ def layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, bet
     """x [M, N] bf16, fp16 or fp32, gamma and beta [N] (x's dtype or fp32, or None) ->
     (y, mean, rstd): y = (x - mean) * rstd * gamma + beta in x's dtype, mean and rstd
     fp32 [M].  `out` may pass (y, mean, rstd) to write into (y may be x)."""
-    code, ldx = _rows(x, "x")
-    M, N = x.shape
-    device = x.get_device()
-    g = b = None
-    pdt = x.dtype
-    if gamma is not None:
-        pdt = gamma.dtype
-        g = _vector(gamma, "gamma", N, (x.dtype, _F32), device)
-    if beta is not None:
-        pdt = pdt if gamma is not None else beta.dtype
-        b = _vector(beta, "beta", N, (pdt,) if gamma is not None else (x.dtype, _F32), device)
     y, mean, rstd = out if out is not None else (None, None, None)
-    y, ldy = (_new_rows(x), N) if y is None else (y, _rows_like(y, "y", x))
-    mean, pm = _given(mean, "mean", M, x, device)
-    rstd, pr = _given(rstd, "rstd", M, x, device)
-    _run(device, "fp8bq_layernorm_forward", x.data_ptr(), M, N, ldx, g, b, eps, y.data_ptr(), ldy, pm, pr, code,
-         _ROW_DTYPES[pdt])
-    return y, mean, rstd
-
-
-NORM_ACCUMULATE = 1
-NORM_RSTD_F64 = 2
-
-
-def _norm_backward(what, dy, x, mean, rstd, gamma, dres, params, out, accumulate):
-    code, ldx = _rows(x, "x")
-    M, N = x.shape
-    device, layernorm = x.get_device(), what == "fp8bq_layernorm_backward"
-    f32 = (_F32,)
-    lddy = _rows_like(dy, "dy", x)
-    dx, dgamma, dbeta = out if out is not None else (None, None, None)
-    dx, lddx = (_new_rows(x), N) if dx is None else (dx, _rows_like(dx, "dx", x))
-    pg = pb = pw = None
-    n = 0
-    if params:
-        if accumulate and (dgamma is None or (layernorm and dbeta is None)):
-            raise ValueError("accumulate=True needs the tensors to add into")
-        dgamma, pg = _given(dgamma, "dgamma", N, x, device)
-        if layernorm:
-            dbeta, pb = _given(dbeta, "dbeta", N, x, device)
-        ws, pw, n = _workspace(device, x, "fp8bq_norm_workspace_bytes", M, N)
-    else:
-        dgamma = dbeta = None
-    args = _CNormGrad(dy.data_ptr(), x.data_ptr(), None if dres is None else dres.data_ptr(), dx.data_ptr(), M, N, lddy, ldx,
-                      0 if dres is None else _rows_like(dres, "dres", x), lddx,
-                      None if gamma is None else _vector(gamma, "gamma", N, (x.dtype, _F32), device),
-                      _vector(mean, "mean", M, f32, device) if layernorm else None,
-                      _vector(rstd, "rstd", M, (_F32, torch.float64), device), pg, pb, pw, n, code,
-                      code if gamma is None else _ROW_DTYPES[gamma.dtype],
-                      (NORM_ACCUMULATE if accumulate else 0) | (NORM_RSTD_F64 if rstd.dtype == torch.float64 else 0), 0)
-    _run(device, what, args)
-    return dx, dgamma, dbeta
+    return (_rows or _row_ops()).layernorm_forward(x, gamma, beta, eps, y, mean, rstd)
 
 
 def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -754,7 +592,8 @@ def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
     `dres` (the residual stream's gradient) added, dgamma and dbeta fp32 [N] (None with
     params=False).  `out` may pass (dx, dgamma, dbeta) to write into; dx may be dy, x or
     dres.  With accumulate=True dgamma and dbeta are added to."""
-    return _norm_backward("fp8bq_layernorm_backward", dy, x, mean, rstd, gamma, dres, params, out, accumulate)
+    dx, dgamma, dbeta = out if out is not None else (None, None, None)
+    return (_rows or _row_ops()).norm_backward(True, dy, x, mean, rstd, gamma, dres, params, dx, dgamma, dbeta, accumulate)
 
 
 def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, gamma: Optional[torch.Tensor] = None,
@@ -762,65 +601,22 @@ def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, gamm
     """The backward pass of h = x * rstd * gamma, with the rstd that rmsnorm_quantize
     returned (fp32, or float64 from exact=True): (dx, dgamma), as layernorm_backward's.
     `out` may pass (dx, dgamma) to write into."""
-    if out is not None:
-        out = (*out, None)
-    return _norm_backward("fp8bq_rmsnorm_backward", dy, x, None, rstd, gamma, dres, params, out, accumulate)[:2]
-
-
-def _dense(t: torch.Tensor) -> bool:
-    """Whether the elements fill one span of memory, in some order."""
-    if t.is_contiguous():
-        return True
-    step = 1
-    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
-        if stride != step:
-            return False
-        step *= size
-    return True
-
-
-def _grad_call(what, grads, out, *more):
-    count = len(grads)
-    if count == 0:
-        raise ValueError("no gradients")
-    if out is not None and len(out) != count:
-        raise ValueError("as many outputs as gradients")
-    device = grads[0].get_device()
-    fields = []  # of an array of fp8bq_grad
-    for g, o in zip(grads, grads if out is None else out):
-        code = _ROW_DTYPES.get(g.dtype)
-        if code is None or g.get_device() != device or device < 0:
-            raise ValueError("the gradients must be bf16, fp16 or fp32 tensors on one CUDA device")
-        plain = g.is_contiguous()
-        if not plain and not _dense(g):
-            raise ValueError("a gradient must fill one span of memory")
-        p = g.data_ptr()
-        if o is g:
-            fields += (p, p, g.numel(), code | code << 32)
-            continue
-        ocode = _ROW_DTYPES.get(o.dtype)
-        if (ocode is None or o.shape != g.shape or o.get_device() != device
-                or not (plain and o.is_contiguous() or o.stride() == g.stride())):
-            raise ValueError("each output must be bf16, fp16 or fp32 of its gradient's shape, strides and device")
-        fields += (p, o.data_ptr(), g.numel(), code | ocode << 32)
-    table = struct.pack(f"={len(fields)}q", *fields)
-    ws, pw, n = _workspace(device, grads[0], "fp8bq_grad_workspace_bytes", count)
-    norm = grads[0].new_empty((), dtype=_F32)
-    _run(device, what, table, count, *more, norm.data_ptr(), pw, n)
-    return norm
+    dx, dgamma = out if out is not None else (None, None)
+    return (_rows or _row_ops()).norm_backward(False, dy, x, None, rstd, gamma, dres, params, dx, dgamma, None,
+                                               accumulate)[:2]
 
 
 def grad_norm(grads) -> torch.Tensor:
     """The 2-norm over all values of a list of bf16, fp16 or fp32 gradients (fp32 scalar on
     the device)."""
-    return _grad_call("fp8bq_grad_norm", grads, None)
+    return (_rows or _row_ops()).grads(grads, None, None)
 
 
 def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     """Scales a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or into the
     list `out` (same shapes; bf16, fp16 or fp32 each), and returns their global norm before
     clipping (fp32 scalar on the device)."""
-    return _grad_call("fp8bq_grad_clip", grads, out, max_norm)
+    return (_rows or _row_ops()).grads(grads, out, max_norm)
 
 
 def set_clock_counters(counters: Optional[torch.Tensor]) -> None:

@@ -312,6 +312,7 @@ def test_norm_refusals():
                 lambda: fp.layernorm_backward(x.half(), x, s, s),
                 lambda: fp.layernorm_backward(x[:, :63], x, s, s),
                 lambda: fp.layernorm_backward(x, x, s[:3], s),
+                lambda: fp.layernorm_backward(x, x, None, s),
                 lambda: fp.layernorm_backward(x, x, s, s, accumulate=True),
                 lambda: fp.rmsnorm_backward(x, x, s.half()),
                 lambda: fp.rmsnorm_backward(x, x, s, out=(x.half(), None))):
