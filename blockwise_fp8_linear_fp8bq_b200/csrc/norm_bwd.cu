@@ -414,29 +414,36 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(const BwdParams p) {
 }
 
 // dgamma and dbeta from the blocks' partial sums, in a fixed order: a block
-// takes 32 columns, its 16 warps every 16th partial each.
-__global__ void __launch_bounds__(512) norm_param_grad_kernel(const float* __restrict__ partial, int64_t parts,
-                                                              int64_t width, int64_t N, float* dgamma, float* dbeta,
-                                                              bool accumulate) {
-  __shared__ float red[16][33];
+// takes 32 columns, its 32 warps every 32nd partial each, eight of them in
+// flight (latency is all there is: a few MB from L2).
+__global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* __restrict__ partial, int64_t parts,
+                                                               int64_t width, int64_t N, float* dgamma, float* dbeta,
+                                                               bool accumulate) {
+  __shared__ float red[32][33];
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
   if (c < width) {
-#pragma unroll 4
-    for (int64_t k = warp; k < parts; k += 16) s += partial[k * width + c];
+    const float* p = partial + c;
+    for (int64_t k0 = warp; k0 < parts; k0 += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = k0 + 32 * i < parts ? p[(k0 + 32 * i) * width] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
   }
   red[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || c >= width) return;
-  s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) s += red[w][lane];
-  float* out = c < N ? dgamma : dbeta;
-  if (out == nullptr) return;
-  out += c < N ? c : c - N;
-  *out = accumulate ? *out + s : s;
+  // warp w adds column w's 32 sums
+  s = warp_sum(red[lane][warp]);
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane != 0 || col >= width) return;
+  if (col < N)
+    write_sum(dgamma, col, s, accumulate);
+  else
+    write_sum(dbeta, col - N, s, accumulate);
 }
 
 // Shared memory for gamma.
@@ -636,7 +643,7 @@ cudaError_t launch_norm_bwd(const fp8bq_norm_grad& a, bool layernorm, cudaStream
   }
   if (!sums || few) return cudaSuccess;
   const int64_t width = a.N * (layernorm ? 2 : 1);
-  return launch_dependent(norm_param_grad_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(512), 0, stream,
+  return launch_dependent(norm_param_grad_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(1024), 0, stream,
                           static_cast<const float*>(a.workspace), blocks, width, a.N, a.dgamma,
                           layernorm ? a.dbeta : nullptr, accumulate);
 }
