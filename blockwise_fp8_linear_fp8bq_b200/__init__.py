@@ -3,8 +3,10 @@
 Every step of the computation runs in the CUDA library ``libfp8bq.so`` (C ABI
 in ``include/fp8bq.h``); this module only allocates outputs with PyTorch,
 marshals pointers and the current CUDA stream, and turns status codes into
-exceptions.  There is no CPU or PyTorch fallback: without the library, or
-without a CUDA device, every call raises.
+exceptions.  (The row operators around the linears -- embedding, LayerNorm,
+norm backward passes, gradient clipping -- do the same in a compiled module,
+_row_binding.so, for their short calls' sake.)  There is no CPU or PyTorch
+fallback: without the library, or without a CUDA device, every call raises.
 
 Method: "Puro-2B: Poor Lab's Qwen2-1.5B Trained on RTX 5090 within $5090"
 (section "方法"): activations quantized in 1x128 groups, weights in 128x128
@@ -634,6 +636,7 @@ def set_clock_counters(counters: Optional[torch.Tensor]) -> None:
 
 
 def check(stream: Optional[torch.cuda.Stream] = None) -> None:
-    """Synchronize and raise if a GEMM kernel's bounded wait expired."""
+    """Synchronize and raise if a kernel's bounded wait expired or an embedding call met an id
+    outside its table."""
     s = stream if stream is not None else torch.cuda.current_stream()
     _raise(lib().fp8bq_check(s.cuda_stream), "fp8bq_check")

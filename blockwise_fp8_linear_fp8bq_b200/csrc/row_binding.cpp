@@ -3,9 +3,10 @@
 // current stream, and the call of the C ABI in include/fp8bq.h.
 //
 // Compiled, unlike the ctypes binding of the other calls, because these
-// operators run for a few microseconds on small batches: checks and three
-// allocations in Python and ctypes' conversion took 9 of LayerNorm's 13 us at
-// [8, 2048].  Nothing is computed here.
+// operators run for a few microseconds on small batches: with checks and
+// allocations in Python and ctypes' conversions, LayerNorm at [8, 2048] took
+// 13.1 us of the host's time, here 7.1 (the launch alone about 3.5).  Nothing
+// is computed here.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
