@@ -130,8 +130,9 @@ __device__ __forceinline__ double norm_of(const double* partial, int64_t parts, 
   return sqrt(block_sum(s, red));
 }
 
-// The factor; NaN where the norm is.
+// The factor; NaN where the norm is, 1 for an infinite limit.
 __device__ __forceinline__ float factor_of(double norm, double max_norm) {
+  if (isinf(max_norm) && !isnan(norm)) return 1.0f;
   const double q = max_norm / (norm + 1e-6);
   return static_cast<float>(q >= 1.0 ? 1.0 : q);
 }

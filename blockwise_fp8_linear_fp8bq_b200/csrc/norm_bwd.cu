@@ -531,7 +531,7 @@ cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
                                              gamma_bytes(b, p.p32 || p.gamma == nullptr ? 4 : sizeof(T)),
                                          std::max<int64_t>(b.groups > 1 ? p.N * (LN ? 8 : 4) : 0,
                                                            columns ? kSliceFloats * 4 : 0));
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
   if (e != cudaSuccess) return e;
   if (columns && p.in_place) {  // the columns are summed before dx is written over them
     BwdParams q = p;

@@ -231,7 +231,7 @@ cudaError_t run_as(FwdParams p, const RowPlan& b, cudaStream_t stream) {
   p.tpr = b.tpr;
   const auto kern = ln_fwd_kernel<T, COLS, SUB, ALIGNED, FULL, SHARED>;
   const int smem = static_cast<int>(b.ring.stage_bytes) * b.ring.stages * b.groups + (SHARED ? b.tpr * COLS * 8 : 0);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(b.blocks), std::max(32, b.tpr) * b.groups, smem, stream>>>(p, b.ring);
   return cudaGetLastError();

@@ -23,6 +23,9 @@ constexpr int kTimeoutRows = 30;
 // of it beside its ring (static arrays and what the system keeps).
 constexpr int64_t kRingBytes = 228 * 1024;
 constexpr int64_t kRingExtra = 3 * 1024;
+// What every kernel with a ring is allowed: one value for all launches, since
+// other host threads may be between setting it and launching.
+constexpr int kMostDynamic = static_cast<int>(kRingBytes - kRingExtra);
 
 struct RingParams {
   const void* src[3];

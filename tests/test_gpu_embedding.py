@@ -82,7 +82,9 @@ def test_ids_outside_the_table(bad):
     (1, 1, 1, 0, "alike"), (2, 3, 64, 0, "alike"), (9, 1031, 640, 8, "uniform"), (100, 7, 77, 1, "uniform"),
     (509, 1031, 640, 0, "text"), (4096, 20, 8, 0, "text"), (4097, 600, 130, 0, "text"), (5000, 2, 48, 0, "alike"),
     (20000, 151936, 64, 0, "text"), (40000, 100000, 16, 0, "text"), (40001, 3, 24, 8, "alike"),
-    (300, 50, 4104, 0, "text"), (33, 500, 8192, 0, "uniform")])
+    (300, 50, 4104, 0, "text"), (33, 500, 8192, 0, "uniform"),
+    (1500, 50, 4104, 0, "text"), (3000, 600000, 8, 0, "uniform"), (6000, 600001, 6, 2, "text"),
+    (1024, 70, 96, 0, "text"), (1025, 70, 96, 0, "text"), (9000, 33, 2050, 0, "text")])
 def test_gradient(T, V, D, pad, kind, dtype, grad):
     gen = gen_of(T + V + D)
     ids = ids_of(gen, T, V, kind, wide=T % 2 == 0)
@@ -109,6 +111,49 @@ def test_gradient(T, V, D, pad, kind, dtype, grad):
     assert_within(got, ref, bound + half_ulp(grad) * (ref.abs() + bound), "dw added")
     assert torch.equal(got[~named], before[~named]) and (buf2[:, D:] == 7.0).all()
     fp.check()
+
+
+@pytest.mark.parametrize("T", [300, 2000, 9000])
+@pytest.mark.parametrize("wide", [False, True])
+def test_padding_and_ids_outside_among_many(T, wide):
+    """Few tokens, one block's sort and the cluster's: ids below 0, at the
+    vocabulary's end and beyond add nothing and are reported, the padding id
+    adds nothing and is not; a padding id outside the table is none."""
+    gen = gen_of(T)
+    V, D = 100, 72
+    ids = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int64 if wide else torch.int32)
+    dy = torch.randn(T, D, generator=gen, device="cuda")
+    dw = fp.embedding_backward(dy, ids, V, padding_id=5)
+    ref, bound = embedding_backward(dy, ids, V, 1.0, 5)
+    assert_within(dw, ref, bound + U * ref.abs(), "dw")
+    assert (dw[5] == 0).all()
+    fp.check()
+    ids[::7], ids[3::7], ids[5::7] = -1, V, V + 1000
+    for padding in (5, V, -3):
+        dw = fp.embedding_backward(dy, ids, V, padding_id=padding)
+        ref, bound = embedding_backward(dy, ids, V, 1.0, padding if padding == 5 else None)
+        assert_within(dw, ref, bound + U * ref.abs(), "dw")
+        with pytest.raises(fp.Fp8bqError) as e:
+            fp.check()
+        assert e.value.status == -7
+
+
+def test_more_values_than_32_bits_count():
+    """A BF16 table of 2.5e9 values (5 GB): rows at its end, and the dense
+    gradient's zeros up to there."""
+    V, D = 151936, 16384
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([V - 1, 0, 131072, V - 2, V - 1], device="cuda")
+    for k, i in enumerate(ids.tolist()):
+        w[i] = k + 1.0
+    assert torch.equal(fp.embedding_forward(w, ids), w[ids])
+    dy = torch.ones(5, D, dtype=torch.bfloat16, device="cuda")
+    w.fill_(3.0)
+    dw = fp.embedding_backward(dy, ids, V, out=w)
+    sums = dw[:, 0].float() + dw[:, D - 1].float()
+    want = torch.zeros(V, device="cuda").index_add_(0, ids, torch.full((5,), 2.0, device="cuda"))
+    assert torch.equal(sums, want)
+    assert sum(dw[v0:v0 + 16384].count_nonzero().item() for v0 in range(0, V, 16384)) == 4 * D
 
 
 def test_gradient_full_size():

@@ -108,6 +108,26 @@ def test_infinities_and_nan():
     assert outs[0].isnan().all() and outs[1].isnan().all()
 
 
+def test_infinite_limit():
+    a, b = torch.ones(3000, device="cuda"), torch.ones(40000, device="cuda")
+    b[7] = float("inf")
+    out = [torch.empty_like(a), torch.empty_like(b)]
+    assert fp.clip_grads([a, b], float("inf"), out=out).item() == float("inf")
+    assert torch.equal(out[0], a) and torch.equal(out[1], b)
+    a[3] = float("nan")
+    fp.clip_grads([a, b], float("inf"), out=out)
+    assert out[0].isnan().all() and out[1].isnan().all()
+
+
+@pytest.mark.parametrize("count,n", [(200, 20000), (129, 1), (128, 5000)])
+def test_more_tensors_than_a_launch_takes(count, n):
+    gen = gen_of(count)
+    grads = [draw(gen, n + k % 7, DTYPES[k % 3]) for k in range(count)]
+    outs = [torch.empty_like(g) for g in grads]
+    norm = fp.clip_grads(grads, 0.3, out=outs)
+    check(grads, norm, outs, 0.3)
+
+
 def test_zero_limit_and_zero_gradients():
     a = torch.ones(1000, device="cuda")
     out = [torch.empty_like(a)]

@@ -124,11 +124,12 @@ def test_two_backward_passes_at_once(M, N):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_layernorm_forward_far_from_zero(dtype):
+@pytest.mark.parametrize("M,N", [(8, 1280), (1500, 100), (1500, 1280), (1500, 1277), (700, 5000), (9, 16384), (8, 20001)])
+def test_layernorm_forward_far_from_zero(M, N, dtype):
     """Rows whose mean is far larger than their spread, constant rows and a
     zero row: y is right to the spread, not to the mean."""
     gen = gen_of(3)
-    x = draw(gen, 8, 1280, dtype, mean=200.0, std=2.0)
+    x = draw(gen, M, N, dtype, mean=200.0, std=2.0)
     x[5] = 3.0
     x[6] = 0.0
     y, mean, rstd = fp.layernorm_forward(x, eps=1e-5)
@@ -260,6 +261,33 @@ def test_rmsnorm_backward_takes_the_producers_rstd(exact):
     assert rstd.dtype == (torch.float64 if exact else torch.float32)
     got = fp.rmsnorm_backward(dy, x, rstd, gamma)
     check_backward("rms", dy, x, None, rstd, gamma, None, (*got, None))
+
+
+def test_statistics_are_optional():
+    """The C call without mean and rstd to write."""
+    x = draw(gen_of(30), 70, 640, torch.bfloat16)
+    want, _, _ = fp.layernorm_forward(x)
+    y = torch.empty_like(x)
+    st = fp.lib().fp8bq_layernorm_forward(x.data_ptr(), 70, 640, 640, None, None, 1e-5, y.data_ptr(), 640, None, None, 1, 1,
+                                          torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(y, want)
+
+
+def test_more_values_than_32_bits_count():
+    """2.25e9 BF16 values (4.5 GB a tensor): the last rows."""
+    M, N = 1100000, 2048
+    x = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    tail = draw(gen_of(31), 300, N, torch.bfloat16)
+    x[-300:] = tail
+    y, mean, rstd = fp.layernorm_forward(x)
+    ry, _, _, bound = layernorm(tail, None, None, 1e-5)
+    assert_within(y[-300:], ry, bound + half_ulp(torch.bfloat16) * (ry.abs() + bound), "y")
+    del y
+    dx, dgamma, dbeta = fp.layernorm_backward(x, x, mean, rstd)  # zero rows add nothing
+    (rdx, bdx), (rdg, bdg), (rdb, bdb) = norm_backward(tail, tail, mean[-300:], rstd[-300:], None, None)
+    assert_within(dx[-300:], rdx, bdx + half_ulp(torch.bfloat16) * (rdx.abs() + bdx), "dx")
+    assert_within(dgamma, rdg, bdg + 8 * U * rdg.abs(), "dgamma")
+    assert_within(dbeta, rdb, bdb + U * rdb.abs(), "dbeta")
 
 
 def test_norm_no_rows():
