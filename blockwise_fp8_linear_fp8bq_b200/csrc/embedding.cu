@@ -5,12 +5,14 @@
 //
 // Both are bound by HBM (16384 tokens, table [151936, 2048] BF16: the lookup
 // takes 17.3 us, 85% of the copy rate; the FP32 gradient 206 us, 97%).  The
-// gradient is summed without floating-point
-// atomics, so equal inputs give equal bits: the tokens are sorted by id (a
-// stable radix sort by one thread-block cluster, while the other SMs write
-// the dense gradient's zeros), equal chunks of the sorted tokens are
-// summed run by run, and a run that spans chunks is joined from its chunks'
-// partial sums in order.
+// gradient is summed without floating-point atomics, so equal inputs give
+// equal bits: the tokens are sorted by id (a stable radix sort by one
+// thread-block cluster, while the other SMs write the dense gradient's zeros),
+// equal chunks of the sorted tokens are summed run by run, and a run that
+// spans chunks is joined from its chunks' partial sums in order.
+//
+// An id outside [0, V) is never used as an address: it is recorded in the
+// status word, which fp8bq_check() reports, and gives zeros or adds nothing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,8 +25,6 @@
 namespace fp8bq {
 namespace {
 
-// Token t's id, or `none` where it is outside [0, V): recorded in the status
-// word, which fp8bq_check() reports.
 __device__ __forceinline__ int64_t load_id(const void* ids, bool i64, int64_t t) {
   return i64 ? static_cast<const int64_t*>(ids)[t] : static_cast<const int32_t*>(ids)[t];
 }

@@ -39,14 +39,7 @@ __device__ __forceinline__ float rstd_of(float var, float eps) {
   return __fdiv_rn(1.0f, __fsqrt_rn(fmaxf(var, 0.0f) + eps));
 }
 
-// A team of tpr threads takes a row at a time (SUB = 8: a team of one warp four
-// rows, 8 lanes each), COLS columns a thread, which stay in registers from one
-// pass to the next.  Teams share nothing but gamma and beta: SHARED keeps
-// those in shared memory, as FP32 pairs, else (few rows, or the longest; one
-// team a block) in registers.  Few threads with many
-// columns, because the sums over a team cost as much for one column as for
-// many: [16384, 2048] BF16 takes 26.5 us (5.1 TB/s, 77% of the copy rate) with
-// one warp a row, 36 us with 128 threads a row and 16 columns each.
+// A sum over each SUB lanes.
 template <int SUB>
 __device__ __forceinline__ float sub_sum(float v) {
 #pragma unroll
@@ -54,6 +47,15 @@ __device__ __forceinline__ float sub_sum(float v) {
   return v;
 }
 
+// A team of tpr threads takes a row at a time (SUB = 8: a team of one warp four
+// rows, 8 lanes each), COLS columns a thread, which stay in registers from one
+// pass to the next.  Teams share nothing but gamma and beta: SHARED keeps
+// those in shared memory, as FP32 pairs, else (few rows, or the longest; one
+// team a block) in registers.  Few threads with many
+// columns, because the sums over a team cost as much for one column as for
+// many; FULL where their columns are the row's, without checks (5-7%):
+// [16384, 2048] BF16 takes 26.5 us (5.1 TB/s, 77% of the copy rate) with
+// one warp a row, 36 us with 128 threads a row and 16 columns each.
 template <class T, int COLS, int SUB, bool ALIGNED, bool FULL, bool SHARED>
 __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const __grid_constant__ FwdParams p,
                                                      const __grid_constant__ RingParams rp) {
@@ -76,6 +78,13 @@ __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const _
   float4* const params = reinterpret_cast<float4*>(smem);  // [COLS / 2][tpr]: a pair's gammas, its betas
   uint8_t* const rings = smem + (SHARED ? COLS / 2 * tpr * static_cast<int>(sizeof(float4)) : 0);
   RowRing<T, 1, ALIGNED> ring(rp, rings + team * rp.stages * rp.stage_bytes, bars[team], &abort_flag, first_row, step);
+  if constexpr (ALIGNED && !FULL) {  // rows are padded with zeros to the threads' columns
+    const int rows = teams * rp.stages * R, tail = static_cast<int>(rp.pitch - rp.row_bytes) / 16;
+    for (int i = tid; i < rows * tail; i += blockDim.x) {
+      const int r = i / tail;
+      *reinterpret_cast<uint4*>(rings + r * rp.pitch + rp.row_bytes + (i - r * tail) * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
   const bool leader = tid == team * members;
   ring.init(leader);
   if (warp == warp0) ring.start();
@@ -115,7 +124,10 @@ __global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const _
     float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      Cols::load(v[j], x, t, tpr, j, n);
+      if constexpr (ALIGNED)
+        Cols::load_padded(v[j], x, t, tpr, j);
+      else
+        Cols::load(v[j], x, t, tpr, j, n);
 #pragma unroll
       for (int i = 0; i < W / 2; i += 2) {
         sum = __fadd2_rn(sum, v[j][i]);
@@ -292,8 +304,10 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
     b.cols = threads(48) * 48 < threads(64) * 64 ? 48 : 64;
     b.tpr = threads(b.cols);
   }
-  const int64_t pitch = aligned || packed ? row : (row + 30) / 16 * 16;
-  const int64_t stage = aligned ? pitch * rows : (pitch * rows + 30) / 16 * 16;
+  const auto pitch_of = [&] {
+    return aligned ? static_cast<int64_t>(b.tpr) * b.cols * size : packed ? row : (row + 30) / 16 * 16;
+  };
+  int64_t pitch = pitch_of(), stage = aligned ? pitch * rows : (pitch * rows + 30) / 16 * 16;
   room = kRingBytes / on_sm - kRingExtra - (shared ? static_cast<int64_t>(b.tpr) * b.cols * 8 : 0);
   b.groups = static_cast<int>(std::min<int64_t>(shared ? 512 / std::max(32, b.tpr) : 1, room / (2 * stage)));
   if (b.groups < 1) {
@@ -303,6 +317,8 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
     b.groups = 1;
     on_sm = 1;
     room = kRingBytes - kRingExtra;
+    pitch = pitch_of();
+    stage = aligned ? pitch : (pitch + 30) / 16 * 16;
     if (room < 2 * stage) return RowPlan{};
   }
   b.rows = rows;
@@ -315,7 +331,7 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
   b.ring.row_bytes = static_cast<uint32_t>(row);
   b.ring.pitch = static_cast<uint32_t>(pitch);
   b.ring.tensor_bytes = b.ring.stage_bytes = static_cast<uint32_t>(stage);
-  b.ring.packed = packed;
+  b.ring.packed = packed && (!aligned || pitch == row);
   return b;
 }
 

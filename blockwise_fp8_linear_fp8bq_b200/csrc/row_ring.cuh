@@ -278,8 +278,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // K sums over the warp at once (K a power of two): halves of the values change
 // places with halves of the lanes, so that K + log2(32 / K) shuffles do the
-// work of 5 K.  A lane with its low bits 0 holds value `index`; warp_sum_of
-// gives every lane value k.
+// work of 5 K.  A lane with its low bits 0 holds value `index`.
 template <int K>
 __device__ __forceinline__ float warp_sums(float (&v)[K], int lane, int& index) {
   int o = 16;
@@ -299,12 +298,8 @@ __device__ __forceinline__ float warp_sums(float (&v)[K], int lane, int& index) 
   for (; o >= 1; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
-template <int K>
-__device__ __forceinline__ float warp_sum_of(float s, int k) {
-  return __shfl_sync(0xffffffffu, s, k * (32 / K));
-}
 
-// The same within each SUB lanes.
+// The same within each SUB lanes; sub_sum_of gives every lane value k.
 template <int K, int SUB>
 __device__ __forceinline__ float sub_sums(float (&v)[K], int lane) {
   int o = SUB / 2;
