@@ -57,7 +57,7 @@ __device__ __forceinline__ float sub_sum(float v) {
 // [16384, 2048] BF16 takes 26.5 us (5.1 TB/s, 77% of the copy rate) with
 // one warp a row, 36 us with 128 threads a row and 16 columns each.
 template <class T, int COLS, int SUB, bool ALIGNED, bool FULL, bool SHARED>
-__global__ void __launch_bounds__(512, COLS <= 16 ? 2 : 1) ln_fwd_kernel(const __grid_constant__ FwdParams p,
+__global__ void __launch_bounds__(512, COLS <= 24 ? 2 : 1) ln_fwd_kernel(const __grid_constant__ FwdParams p,
                                                      const __grid_constant__ RingParams rp) {
   constexpr int W = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 8, G = COLS / W;
   constexpr int R = 32 / SUB;  // rows a team takes at a time
@@ -267,6 +267,8 @@ cudaError_t run_plan(const FwdParams& p, const RowPlan& b, cudaStream_t stream) 
     case 8: return run<T, 8, 32, ALIGNED, false>(p, b, stream);
     case 16: return run<T, 16, 32, ALIGNED, true>(p, b, stream);
     case 32: return b.tpr == 32 ? run<T, 32, 32, ALIGNED, true>(p, b, stream) : run<T, 32, 32, ALIGNED, false>(p, b, stream);
+    case 24: return run<T, 24, 32, ALIGNED, true>(p, b, stream);
+    case 40: return run<T, 40, 32, ALIGNED, true>(p, b, stream);
     case 48: return run<T, 48, 32, ALIGNED, true>(p, b, stream);
     default: return run<T, 64, 32, ALIGNED, true>(p, b, stream);
   }
@@ -297,9 +299,9 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
     rows = 4;
     on_sm = b.cols <= 16 ? 2 : 1;
   } else if (N <= 2048) {
-    b.cols = N <= 512 ? 16 : N <= 1024 ? 32 : N <= 1536 ? 48 : 64;
+    b.cols = N <= 512 ? 16 : N <= 768 ? 24 : N <= 1024 ? 32 : N <= 1280 ? 40 : N <= 1536 ? 48 : 64;
     b.tpr = 32;
-    on_sm = b.cols <= 16 ? 2 : 1;
+    on_sm = b.cols <= 24 ? 2 : 1;
   } else {
     b.cols = threads(48) * 48 < threads(64) * 64 ? 48 : 64;
     b.tpr = threads(b.cols);

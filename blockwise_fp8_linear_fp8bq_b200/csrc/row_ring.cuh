@@ -244,11 +244,13 @@ struct Group {
 
   // Zeros in the place of values past the row.
   __device__ static __forceinline__ void clear_rest(float2 (&v)[W / 2], int t, int stride, int j, int n) {
-    if (FULL || whole(stride, j, n)) return;
+    if constexpr (!FULL) {
+      if (whole(stride, j, n)) return;
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      if (column(t, stride, j, 2 * i) >= n) v[i].x = 0.0f;
-      if (column(t, stride, j, 2 * i + 1) >= n) v[i].y = 0.0f;
+      for (int i = 0; i < W / 2; ++i) {
+        if (column(t, stride, j, 2 * i) >= n) v[i].x = 0.0f;
+        if (column(t, stride, j, 2 * i + 1) >= n) v[i].y = 0.0f;
+      }
     }
   }
 
