@@ -262,7 +262,9 @@ cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm
     parts += blocks;
     chunks += t.chunks;
   }
-  const bool many = chunks > 4 * static_cast<int64_t>(sms);
+  // Many chunks: the factor by a kernel of its own (10 M FP32 values: 24.1 us
+  // against 24.8; 4 M: 12.7 against 12.4; 1 M: 6.6 against 5.7).
+  const bool many = chunks > 8 * static_cast<int64_t>(sms);
   if (!clip || parts == 0 || many) {
     e = launch_dependent(norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(partial), parts, max_norm,
                          norm, clip ? factor : nullptr);

@@ -10,10 +10,9 @@
 // go to the workspace and are added in a fixed order by a second kernel.
 // [16384, 2048] BF16 with a residual: LayerNorm 51 us (5.3 TB/s, 80% of the copy
 // rate), RMSNorm 48 (85%); the first kernel, which loaded rows straight into
-// registers, took 94 and 86, waiting for them.  Few
-// rows (small_batch) leave those sums to further blocks of the same launch,
-// which read x and dy again, from L2: one launch instead of two, and no
-// workspace.
+// registers, took 94 and 86, waiting for them.  Few rows (small_batch) leave
+// those sums to further blocks of the same launch, which read x and dy again,
+// from L2: one launch instead of two, and no workspace.
 //
 // Included by one source for each element type (they compile side by side) and
 // by norm_bwd.cu, which lays the launches out.

@@ -51,11 +51,11 @@ __device__ __forceinline__ float sub_sum(float v) {
 // rows, 8 lanes each), COLS columns a thread, which stay in registers from one
 // pass to the next.  Teams share nothing but gamma and beta: SHARED keeps
 // those in shared memory, as FP32 pairs, else (few rows, or the longest; one
-// team a block) in registers.  Few threads with many
-// columns, because the sums over a team cost as much for one column as for
-// many; FULL where their columns are the row's, without checks (5-7%):
-// [16384, 2048] BF16 takes 26.5 us (5.1 TB/s, 77% of the copy rate) with
-// one warp a row, 36 us with 128 threads a row and 16 columns each.
+// team a block) in registers.  Few threads with many columns, because the sums
+// over a team cost as much for one column as for many: [16384, 2048] BF16
+// takes 26.3 us (5.1 TB/s, 78% of the copy rate) with one warp a row, 36 us
+// with 128 threads a row and 16 columns each.  FULL: the threads' columns are
+// the row's, without checks (5-7% faster than zero padding).
 template <class T, int COLS, int SUB, bool ALIGNED, bool FULL, bool SHARED>
 __global__ void __launch_bounds__(512, COLS <= 24 ? 2 : 1) ln_fwd_kernel(const __grid_constant__ FwdParams p,
                                                      const __grid_constant__ RingParams rp) {
@@ -274,8 +274,10 @@ cudaError_t run_plan(const FwdParams& p, const RowPlan& b, cudaStream_t stream) 
   }
 }
 
-// Few rows: a block each, 8 columns a thread ([200, 1283] FP32 4.7 us; the
-// teams below, which first bring gamma and beta to shared memory, 6.9).
+// Few rows, not too long: a block each, 8 columns a thread ([200, 1283] FP32
+// 4.7 us; the teams below, which first bring gamma and beta to shared memory,
+// 6.9; [290, 640] FP32 3.6 and 4.9, [290, 4096] BF16 4.8 and 4.2, [600, 2048]
+// 6.3 and 4.2).
 // Rows of up to 256 columns: 8 lanes each.  Else teams of one warp where 64
 // columns a thread hold the row, or the team and columns (48 or 64) that leave
 // the fewest idle; as many teams a block, up to 16 warps, as leave each two
@@ -288,7 +290,7 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
   int64_t room = kRingBytes - kRingExtra;
   int on_sm = 1, rows = 1;  // blocks that the registers allow; rows a team takes at a time
   bool shared = true;
-  if (M <= 2 * sms && N <= 512 * 8) {
+  if (M <= 2 * sms && N <= 256 * 8) {
     b.cols = 8;
     b.tpr = threads(8);
     on_sm = 2;

@@ -3,10 +3,11 @@
 //
 // A team (a block, or some warps of one) takes `rows` consecutive rows of
 // every tensor at a time (a row block); bulk copies bring its next row blocks
-// into the stages of its ring while the current one is worked on.  Rows that are not 16-byte aligned are
-// fetched as the 16-byte granules that hold them and read from shared memory
-// value by value; the granules at a tensor's two ends, which may reach past
-// it, are copied value by value instead.  Every wait is bounded.
+// into the stages of its ring while the current one is worked on.  Rows that
+// are not 16-byte aligned are fetched as the 16-byte granules that hold them
+// and read from shared memory value by value; the granules at a tensor's two
+// ends, which may reach past it, are copied value by value instead.  Every
+// wait is bounded.
 #pragma once
 #include <algorithm>
 #include <cstdint>

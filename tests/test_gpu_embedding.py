@@ -116,7 +116,7 @@ def test_gradient(T, V, D, pad, kind, dtype, grad):
 @pytest.mark.parametrize("T", [300, 2000, 9000])
 @pytest.mark.parametrize("wide", [False, True])
 def test_padding_and_ids_outside_among_many(T, wide):
-    """Few tokens, one block's sort and the cluster's: ids below 0, at the
+    """Few tokens, the sort: ids below 0, at the
     vocabulary's end and beyond add nothing and are reported, the padding id
     adds nothing and is not; a padding id outside the table is none."""
     gen = gen_of(T)
