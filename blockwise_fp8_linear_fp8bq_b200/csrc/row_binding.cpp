@@ -5,7 +5,7 @@
 // Compiled, unlike the ctypes binding of the other calls, because these
 // operators run for a few microseconds on small batches: with checks and
 // allocations in Python and ctypes' conversions, LayerNorm at [8, 2048] took
-// 13.1 us of the host's time, here 7.1 (the launch alone about 3.5).  Nothing
+// 13.1 us of the host's time, here 6.1 (the launch alone about 3.5).  Nothing
 // is computed here.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>

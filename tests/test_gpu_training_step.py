@@ -86,3 +86,18 @@ def test_training_step():
     fp.check()
     assert torch.equal(captured["norm"], r["norm"])
     assert all(torch.equal(a, b) for a, b in zip(captured["clipped"], r["clipped"]))
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_on_a_device_that_is_not_current():
+    """Tensors of another device than the current one: the calls run there."""
+    with torch.cuda.device(1):
+        x = torch.randn(300, 640, device="cuda").to(BF)
+        ids = torch.randint(0, 50, (300,), device="cuda")
+        y, mean, rstd = fp.layernorm_forward(x)
+        want = (y, mean, rstd, *fp.layernorm_backward(x, x, mean, rstd), fp.embedding_backward(x, ids, 50), fp.grad_norm([x]))
+    y, mean, rstd = fp.layernorm_forward(x)
+    got = (y, mean, rstd, *fp.layernorm_backward(x, x, mean, rstd), fp.embedding_backward(x, ids, 50), fp.grad_norm([x]))
+    assert torch.cuda.current_device() == 0
+    torch.cuda.synchronize(1)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
