@@ -45,6 +45,7 @@ struct LookupParams {
 template <class W, class Y, int VEC>
 __global__ void __launch_bounds__(256) lookup_kernel(const LookupParams p) {
   constexpr int kPacks = 4;
+  cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t t = warp / p.pieces;
@@ -82,10 +83,8 @@ cudaError_t run_lookup(LookupParams p, cudaStream_t stream) {
   const int64_t blocks = (p.T * p.pieces + 7) / 8;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (wide)
-    lookup_kernel<W, Y, kVec><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
-  else
-    lookup_kernel<W, Y, 1><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+    return launch_dependent(lookup_kernel<W, Y, kVec>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p);
+  return launch_dependent(lookup_kernel<W, Y, 1>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p);
 }
 
 template <class W>
@@ -137,7 +136,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
   extern __shared__ uint32_t count[];  // [kSortWarps][kBins]
   __shared__ uint32_t total[kBins], base[kBins], scan[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  cudaTriggerProgrammaticLaunchCompletion();  // the zeros need no result of this kernel
+  cudaGridDependencySynchronize();
+  // the zeros need no result of this kernel, only that what came before it is done
+  cudaTriggerProgrammaticLaunchCompletion();
   const uint32_t rank = cluster_ctarank();
   uint32_t* mine = count + warp * kBins;
   const int64_t begin = (static_cast<int64_t>(rank) * kSortWarps + warp) * p.per_warp;
@@ -425,6 +426,7 @@ template <class T, class G, int VEC>
 __global__ void __launch_bounds__(256) grad_few_kernel(const FewParams p) {
   __shared__ int list[kFewTokens], counts[8];
   __shared__ uint8_t named[kFewRows];
+  cudaGridDependencySynchronize();
   const GradParams& g = p.g;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T_ = static_cast<int>(g.T);
   if (blockIdx.x >= static_cast<unsigned>(T_)) {
@@ -537,10 +539,8 @@ cudaError_t grad_of_type(const FewParams& f, bool few, cudaStream_t stream) {
   const int64_t zeros = p.accumulate ? 0 : (f.z.V + f.z.rows - 1) / f.z.rows;
   const unsigned blocks = static_cast<unsigned>(p.T + zeros);
   if (wide)
-    grad_few_kernel<T, G, kVec><<<blocks, 256, 0, stream>>>(f);
-  else
-    grad_few_kernel<T, G, 1><<<blocks, 256, 0, stream>>>(f);
-  return cudaGetLastError();
+    return launch_dependent(grad_few_kernel<T, G, kVec>, dim3(blocks), dim3(256), 0, stream, f);
+  return launch_dependent(grad_few_kernel<T, G, 1>, dim3(blocks), dim3(256), 0, stream, f);
 }
 
 cudaError_t grad_of_types(const FewParams& f, int dtype, int dw_dtype, bool few, cudaStream_t stream) {
@@ -627,13 +627,15 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kSortCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, sort_kernel, s);
   if (e != cudaSuccess) return e;
   if (!a.accumulate) {

@@ -108,6 +108,7 @@ __device__ __forceinline__ double block_sum(double s, double* red) {
 
 __global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant__ Table t, double* partial) {
   __shared__ double red[kThreads / 32];
+  cudaGridDependencySynchronize();
   double s = 0.0;
   for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const int i = tensor_of(t, k);
@@ -256,8 +257,7 @@ cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm
     at = fill_table(grads, count, at, &t);
     if (t.chunks == 0) break;
     const int64_t blocks = blocks_of(t.chunks, sms);
-    square_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(t, partial + parts);
-    e = cudaGetLastError();
+    e = launch_dependent(square_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, t, partial + parts);
     if (e != cudaSuccess) return e;
     parts += blocks;
     chunks += t.chunks;

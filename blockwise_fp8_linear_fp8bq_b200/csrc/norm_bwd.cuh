@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
   using Cols = Group<T, W, ALIGNED, false, false>;
   using Sums = Group<float, W, ALIGNED, false, false>;
   extern __shared__ __align__(128) uint8_t smem[];
+  cudaGridDependencySynchronize();
   if (blockIdx.x >= static_cast<unsigned>(p.row_blocks)) {
     column_block<T, LN, ALIGNED>(p, reinterpret_cast<float*>(smem));
     return;
@@ -450,7 +451,7 @@ cudaError_t run_as(BwdParams p, const RowPlan& b, cudaStream_t stream) {
     kern<<<static_cast<unsigned>(slices), b.tpr * b.groups, smem, stream>>>(q, b.ring);
     kern<<<static_cast<unsigned>(b.blocks), b.tpr * b.groups, smem, stream>>>(p, b.ring);
   } else {
-    kern<<<static_cast<unsigned>(b.blocks + slices), b.tpr * b.groups, smem, stream>>>(p, b.ring);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks + slices)), dim3(b.tpr * b.groups), smem, stream, p, b.ring);
   }
   return cudaGetLastError();
 }

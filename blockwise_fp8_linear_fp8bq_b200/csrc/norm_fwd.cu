@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(512, COLS <= 24 ? 2 : 1) ln_fwd_kernel(const _
   const int tpr = SUB < 32 ? SUB : p.tpr, t = SUB < 32 ? lane % SUB : tid - team * members;  // threads a row
   const int warps = members >> 5, warp0 = team * warps;
   const int n = rp.n;
+  cudaGridDependencySynchronize();
 
   // rows over the SMs first
   const int64_t first_row = (blockIdx.x + static_cast<int64_t>(gridDim.x) * team) * R;
@@ -245,8 +246,8 @@ cudaError_t run_as(FwdParams p, const RowPlan& b, cudaStream_t stream) {
   const int smem = static_cast<int>(b.ring.stage_bytes) * b.ring.stages * b.groups + (SHARED ? b.tpr * COLS * 8 : 0);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(b.blocks), std::max(32, b.tpr) * b.groups, smem, stream>>>(p, b.ring);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks)), dim3(std::max(32, b.tpr) * b.groups), smem, stream, p,
+                          b.ring);
 }
 
 template <class T, int COLS, int SUB, bool ALIGNED, bool SHARED>

@@ -88,6 +88,77 @@ def test_training_step():
     assert all(torch.equal(a, b) for a, b in zip(captured["clipped"], r["clipped"]))
 
 
+def test_behind_copies_and_fills():
+    """Each operator right behind a host copy, a fill and another operator that
+    writes its inputs, eagerly, on a side stream and captured: none reads or
+    writes ahead of what comes before it on the stream."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    M, N, V = 3000, 1024, 700
+    sources = [torch.randn(M, N, generator=gen, device="cuda").to(BF).cpu().pin_memory() for _ in range(3)]
+    id_sources = [torch.randint(0, V, (M,), generator=gen, device="cuda").cpu().pin_memory() for _ in range(3)]
+    x, ids = torch.empty(M, N, dtype=BF, device="cuda"), torch.empty(M, dtype=torch.int64, device="cuda")
+    host_x, host_ids = torch.empty(M, N, dtype=BF).pin_memory(), torch.empty(M, dtype=torch.int64).pin_memory()
+    dw, dx = torch.empty(V, N, device="cuda"), torch.empty(M, N, dtype=BF, device="cuda")
+    big = torch.empty(64 << 20, device="cuda")
+
+    def run():
+        big.fill_(1.0)  # work that is still running when the rest is queued
+        x.copy_(host_x, non_blocking=True)
+        y, mean, rstd = fp.layernorm_forward(x)
+        dx.fill_(7.0)
+        fp.layernorm_backward(y, x, mean, rstd, out=(dx, None, None), params=False)
+        ids.copy_(host_ids, non_blocking=True)
+        dw.fill_(7.0)
+        fp.embedding_backward(dx, ids, V, out=dw)
+        t = fp.embedding_forward(dw, ids)
+        dw.mul_(0.5)
+        fp.embedding_backward(dx, ids, V, out=dw, accumulate=True)
+        norm = fp.clip_grads([dw, t], 1.0)
+        return y, dx.clone(), t, norm, dw.clone()
+
+    def plain():
+        y, mean, rstd = fp.layernorm_forward(x)
+        torch.cuda.synchronize()
+        a = fp.layernorm_backward(y, x, mean, rstd, params=False)[0]
+        torch.cuda.synchronize()
+        w = fp.embedding_backward(a, ids, V)
+        torch.cuda.synchronize()
+        t = fp.embedding_forward(w, ids)
+        w = w * 0.5
+        torch.cuda.synchronize()
+        fp.embedding_backward(a, ids, V, out=w, accumulate=True)
+        torch.cuda.synchronize()
+        norm = fp.clip_grads([w, t], 1.0)
+        torch.cuda.synchronize()
+        return y, a, t, norm, w
+
+    def fill(k):
+        torch.cuda.synchronize()
+        host_x.copy_(sources[k])
+        host_ids.copy_(id_sources[k])
+
+    fill(0)
+    got = run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, plain()))
+    fill(1)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = run()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, plain()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for k in (2, 0):
+        fill(k)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, plain()))
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
 def test_on_a_device_that_is_not_current():
     """Tensors of another device than the current one: the calls run there."""
