@@ -187,7 +187,7 @@ int grad_list(const fp8bq_grad* grads, int count, double max_norm, bool clip, fl
     const fp8bq_grad& g = grads[i];
     const int64_t e = elem_bytes(g.dtype), o = clip ? elem_bytes(g.out_dtype) : 1;
     if (e == 0 || o == 0) return FP8BQ_ERR_INVALID_ARG;
-    if (g.n < 0 || g.n > (int64_t{1} << 36)) return FP8BQ_ERR_SHAPE;
+    if (g.n < 0 || g.n > (int64_t{1} << 35)) return FP8BQ_ERR_SHAPE;
     if (g.n > 0 && (!g.g || (clip && !g.out))) return FP8BQ_ERR_INVALID_ARG;
     if (clip && g.n > 0 && g.g == g.out && g.dtype != g.out_dtype) return FP8BQ_ERR_INVALID_ARG;
     if (!aligned_to(g.g, e) || (clip && !aligned_to(g.out, o))) return FP8BQ_ERR_ALIGN;

@@ -26,6 +26,8 @@ constexpr int kUnits = 2;                     // units of a chunk
 constexpr int kChunk = kUnits * kUnit;        // values of one tensor a block takes before it looks for more
 constexpr int kNormBlocks = 8;                // blocks for each SM that take the norm
 constexpr int kTensors = 128;                 // tensors a launch takes (its parameters hold their table)
+// A launch's chunks fit a grid: at most 2^35 values a tensor.
+static_assert((int64_t{1} << 35) / kChunk * kTensors <= INT32_MAX, "chunks of a launch");
 
 struct Table {
   const void* g[kTensors];
@@ -274,7 +276,6 @@ cudaError_t launch_grad_clip(const fp8bq_grad* grads, int count, double max_norm
   for (int at = 0; at < count;) {
     at = fill_table(grads, count, at, &t);
     if (t.chunks == 0) break;
-    if (t.chunks > INT32_MAX) return cudaErrorInvalidValue;
     e = launch_dependent(scale_kernel, dim3(static_cast<unsigned>(t.chunks)), dim3(kThreads), 0, stream, t,
                          static_cast<const double*>(partial), parts, max_norm, first ? norm : nullptr,
                          many ? static_cast<const float*>(factor) : nullptr);

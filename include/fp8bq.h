@@ -393,7 +393,7 @@ int64_t fp8bq_norm_workspace_bytes(int64_t M, int64_t N);
  * Errors: as above; ERR_INVALID_ARG for a max_norm below 0 or NaN, an out
  * that is g with another dtype or that overlaps another tensor of the list
  * (a tensor listed twice among them), or a workspace too small; ERR_SHAPE
- * for count < 0 or n outside 0 .. 2^36.
+ * for count < 0 or n outside 0 .. 2^35.
  */
 typedef struct fp8bq_grad {
   const void* g;
