@@ -121,6 +121,7 @@ struct RowRing {
         if (head > 0 || tail < count) fence_proxy_async_smem();  // a later copy may write these bytes
       }
       total = __reduce_add_sync(0xffffffffu, total);
+      __syncwarp();  // every lane's values are in the stage before lane 0 announces it (the sum orders no memory)
       if (lane == 0) mbar_arrive_expect_tx(bar, total);
       __syncwarp();
       for (int i = lane; i < copies; i += 32) {

