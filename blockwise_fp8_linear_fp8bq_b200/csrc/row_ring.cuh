@@ -89,7 +89,10 @@ struct RowRing {
   __device__ __forceinline__ void fetch() {
     const int lane = threadIdx.x & 31;
     const int64_t row0 = fetch_row;
-    if (row0 >= p.M || *static_cast<volatile int*>(abort_flag) != 0) return;
+    if (row0 >= p.M) return;
+    // one lane's reading for the warp: another team may set the flag meanwhile,
+    // and lanes that left would be waited for below
+    if (__shfl_sync(0xffffffffu, lane == 0 ? *static_cast<volatile int*>(abort_flag) : 0, 0) != 0) return;
     const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.M - row0));
     const uint32_t bar = smem_u32(&bars[fetch_stage]);
     uint8_t* base = ring + fetch_stage * p.stage_bytes;
