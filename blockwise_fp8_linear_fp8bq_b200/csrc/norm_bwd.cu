@@ -14,9 +14,8 @@ namespace {
 // dgamma and dbeta from the blocks' partial sums, in a fixed order: a block
 // takes 32 columns, its 32 warps every 32nd partial each, eight of them in
 // flight (latency is all there is: a few MB from L2).
-__global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* __restrict__ partial, int64_t parts,
-                                                               int64_t width, int64_t N, float* dgamma, float* dbeta,
-                                                               bool accumulate) {
+__global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* partial, int64_t parts, int64_t width,
+                                                               int64_t N, float* dgamma, float* dbeta, bool accumulate) {
   __shared__ float red[32][33];
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -1,11 +1,13 @@
-"""What no run can show of the row ring's fetch: the hardware's order hides a
-missing barrier, and a lane that leaves alone needs another warp's wait to expire
-at that moment.  The source is read instead."""
+"""What no run can show of the row operators' kernels: the hardware's order hides
+a missing barrier, a lane that leaves alone needs another warp's wait to expire at
+that moment, and a promise to the compiler that does not hold need not be used.
+The sources are read instead."""
+import glob
 import os
 import re
 
-SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "blockwise_fp8_linear_fp8bq_b200",
-                      "csrc", "row_ring.cuh")
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "blockwise_fp8_linear_fp8bq_b200", "csrc")
+SOURCE = os.path.join(CSRC, "row_ring.cuh")
 
 
 def fetch_body():
@@ -25,3 +27,13 @@ def test_a_warp_leaves_together():
     reads = [m.start() for m in re.finditer("abort_flag", body)]
     assert len(reads) == 1
     assert re.search(r"__shfl_sync\([^;]*abort_flag[^;]*, 0\) != 0\) return;", body)
+
+
+def test_early_kernels_promise_no_constant_memory():
+    """A kernel that may start before the one that writes its inputs has ended."""
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for kernel in re.finditer(r"__global__[^;{]*\{", text):
+            body = text[kernel.end():text.find("\n}\n", kernel.end())]
+            if "cudaGridDependencySynchronize" in body:
+                assert "__restrict__" not in kernel.group(0) and "__ldg" not in body, kernel.group(0)
