@@ -79,7 +79,7 @@ cudaError_t run_lookup(LookupParams p, cudaStream_t stream) {
   constexpr int kVec = 16 / static_cast<int>(std::min(sizeof(W), sizeof(Y)));
   const bool wide = p.D % kVec == 0 && rows_aligned(p.w, p.ldw, sizeof(W), 16) && rows_aligned(p.y, p.ldy, sizeof(Y), 16);
   const int piece = 128 * (wide ? kVec : 1);
-  p.pieces = (p.D + piece - 1) / piece;
+  p.pieces = static_cast<int>((static_cast<int64_t>(p.D) + piece - 1) / piece);
   const int64_t blocks = (p.T * p.pieces + 7) / 8;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (wide)
@@ -286,7 +286,7 @@ struct GradParams {
 };
 
 template <class G, int VEC>
-__device__ __forceinline__ void write_row(const GradParams& p, int64_t row, int c, const float (&acc)[VEC]) {
+__device__ __forceinline__ void write_row(const GradParams& p, int64_t row, int64_t c, const float (&acc)[VEC]) {
   G* dst = static_cast<G*>(p.dw) + row * p.lddw + c;
   Pack<G, VEC> o;
   if (p.accumulate) {
@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p) {
     last += more;
     if (more < 32) break;
   }
-  for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC; c < p.D; c += gridDim.y * blockDim.x * VEC) {
+  const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.x * VEC;
+  for (int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * VEC; c < p.D; c += step) {
     const float* src = p.partial + c;
     float acc[VEC];
     Pack<float, VEC> v;
@@ -510,7 +511,7 @@ int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 template <class T, class G, int VEC>
 cudaError_t run_grad(GradParams p, cudaStream_t stream) {
-  const int slots = (p.D + VEC - 1) / VEC;
+  const int64_t slots = (static_cast<int64_t>(p.D) + VEC - 1) / VEC;
   p.cols = 1;
   while (p.cols < slots && p.cols < 256) p.cols *= 2;
   const int rows = 256 / p.cols;
@@ -518,8 +519,10 @@ cudaError_t run_grad(GradParams p, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((slots + p.cols - 1) / p.cols), static_cast<unsigned>((p.chunks + rows - 1) / rows));
   cudaError_t e = launch_dependent(grad_chunk_kernel<T, G, VEC>, grid, dim3(256), 0, stream, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
-  const int threads = std::min(256, (slots + 31) / 32 * 32);
-  const dim3 join(static_cast<unsigned>(p.chunks - 1), static_cast<unsigned>((slots + threads - 1) / threads));
+  const int threads = static_cast<int>(std::min<int64_t>(256, (slots + 31) / 32 * 32));
+  // a grid's second dimension ends at 65535: blocks of longer rows take several pieces
+  const int64_t pieces = std::min<int64_t>(65535, (slots + threads - 1) / threads);
+  const dim3 join(static_cast<unsigned>(p.chunks - 1), static_cast<unsigned>(pieces));
   return launch_dependent(grad_join_kernel<G, VEC>, join, dim3(threads), 0, stream, p);
 }
 

@@ -54,3 +54,22 @@ def test_values_at_the_ends_of_unaligned_tensors(M, N, dtype, kind):
             dx = backward(kind, dy, x, mean, rstd, None, dres)[0]
             assert_within(dx, ref, bound + half_ulp(dtype) * (ref.abs() + bound), "dx")
     fp.check()
+
+
+def test_table_gradient_of_rows_longer_than_a_grids_second_dimension():
+    """Rows of an odd length of which a grid of 65535 x 256 threads does not reach
+    the end, in two chunks of tokens that one id's run spans."""
+    T, V, D = 9, 2, 65535 * 256 + 300001
+    ids = torch.tensor([0, 1, 1, 1, 1, 1, 1, 1, 1], device="cuda")  # the last of them is the second chunk
+    dy = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    for t in range(T):
+        dy[t] = t + 1.0
+        dy[t, -1] = -1.0 - t
+    dw = fp.embedding_backward(dy, ids, V, scale=0.5)
+    for v, s in ((0, 0.5), (1, 22.0)):
+        assert (dw[v, :-1] == s).all() and dw[v, -1] == -s
+    fp.embedding_backward(dy, ids, V, scale=0.5, out=dw, accumulate=True)
+    for v, s in ((0, 1.0), (1, 44.0)):
+        assert (dw[v, :-1] == s).all() and dw[v, -1] == -s
+    fp.check()
+    torch.cuda.synchronize()
