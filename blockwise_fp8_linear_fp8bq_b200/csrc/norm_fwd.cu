@@ -287,13 +287,13 @@ cudaError_t run_plan(const FwdParams& p, const RowPlan& b, cudaStream_t stream) 
 RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, int sms) {
   RowPlan b{};
   const int64_t row = N * size;
-  const auto threads = [&](int cols) { return static_cast<int>(((N + cols - 1) / cols + 31) / 32 * 32); };
+  const auto threads = [&](int cols) { return ((N + cols - 1) / cols + 31) / 32 * 32; };
   int64_t room = kRingBytes - kRingExtra;
   int on_sm = 1, rows = 1;  // blocks that the registers allow; rows a team takes at a time
   bool shared = true;
   if (M <= 2 * sms && N <= 256 * 8) {
     b.cols = 8;
-    b.tpr = threads(8);
+    b.tpr = static_cast<int>(threads(8));
     on_sm = 2;
     shared = false;
   } else if (N <= 256) {
@@ -307,7 +307,7 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
     on_sm = b.cols <= 24 ? 2 : 1;
   } else {
     b.cols = threads(48) * 48 < threads(64) * 64 ? 48 : 64;
-    b.tpr = threads(b.cols);
+    b.tpr = static_cast<int>(threads(b.cols));
   }
   const auto pitch_of = [&] {
     return aligned ? static_cast<int64_t>(b.tpr) * b.cols * size : packed ? row : (row + 30) / 16 * 16;
@@ -318,7 +318,7 @@ RowPlan plan_fwd(int64_t M, int64_t N, int64_t size, bool aligned, bool packed, 
   if (b.groups < 1) {
     if (threads(32) > 512) return RowPlan{};
     b.cols = 32;
-    b.tpr = threads(32);
+    b.tpr = static_cast<int>(threads(32));
     b.groups = 1;
     on_sm = 1;
     room = kRingBytes - kRingExtra;
