@@ -292,12 +292,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
       return __shfl_sync(0xffffffffu, sum, k % 32);
     };
     sum *= -p.inv_n;
-    // dx = rstd * g + (-rstd * c1) + (x - mean) * (-rstd^2 * c2)
+    // dx = rstd * (g - c1 - xh * c2): rstd stays a factor of its own on either
+    // side, since rstd^2 leaves FP32's range long before x, rstd and dx do
     T* dx = static_cast<T*>(p.dx) + row0 * p.lddx;
 #pragma unroll
     for (int r = 0; r < R; ++r, dx += p.lddx) {
-      const float k2 = value(r) * rstd[r] * rstd[r];
-      const float k1 = LN ? value(R + r) * rstd[r] : 0.0f;
+      const float k2 = value(r), k1 = LN ? value(R + r) : 0.0f;
       if (SUB == 32 && r >= live) break;  // (SUB < 32: the warp's other rows may live)
       const float2 c1 = make_float2(k1, k1), c2 = make_float2(k2, k2), rs = make_float2(rstd[r], rstd[r]);
       const T* sx = ring.row(0, block_row, group * R + r);
@@ -312,10 +312,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ B
         if constexpr (!kGammaRegs) kept_gamma(gj, j);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
-          const float2 g = __fmul2_rn(y[i], kGammaRegs ? gam[kGammaRegs ? j : 0][i] : gj[i]);
-          float2 d = LN ? __ffma2_rn(__fadd2_rn(x[i], mean[r]), c2, c1) : __fmul2_rn(x[i], c2);
-          d = __ffma2_rn(g, rs, d);
-          x[i] = RES ? __fadd2_rn(d, z[i]) : d;
+          const float2 gi = kGammaRegs ? gam[kGammaRegs ? j : 0][i] : gj[i];
+          const float2 xh = __fmul2_rn(LN ? __fadd2_rn(x[i], mean[r]) : x[i], rs);
+          float2 d = LN ? __ffma2_rn(xh, c2, c1) : __fmul2_rn(xh, c2);
+          d = __ffma2_rn(y[i], gi, d);
+          x[i] = RES ? __ffma2_rn(d, rs, z[i]) : __fmul2_rn(d, rs);
         }
         if (SUB == 32 || r < live) Cols::store(dx, x, t, tpr, j, n);
       }

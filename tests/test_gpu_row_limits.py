@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import blockwise_fp8_linear_fp8bq_b200 as fp
-from row_ref import assert_within, half_ulp, layernorm, norm_backward
+from row_ref import U, assert_within, half_ulp, layernorm, norm_backward
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,36 @@ def test_table_gradient_of_rows_longer_than_a_grids_second_dimension():
         assert (dw[v, :-1] == s).all() and dw[v, -1] == -s
     fp.check()
     torch.cuda.synchronize()
+
+
+# (rows, columns): one warp's, 8 lanes', several warps', few rows', unaligned and long rows
+LAYOUTS = [(1100, 640), (1100, 64), (1100, 100), (1050, 4096), (1100, 641), (40, 2048), (40, 77), (20, 20001)]
+
+
+@pytest.mark.parametrize("kind", ["ln", "rms", "rms64"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N", LAYOUTS + [(1030, 2047), (1100, 2048), (300, 12288)])
+def test_norm_backward_of_tiny_and_huge_rows(M, N, dtype, kind):
+    """Rows whose rstd is in FP32's range and whose rstd^2 is not (eps = 0 for the
+    tiny ones); dy goes along with x, so that the projection is as large as dy.
+    rms64: a float64 rstd."""
+    gen = gen_of(M + N)
+    x0 = torch.randn(M, N, generator=gen, device="cuda") + 0.3
+    dy0 = 0.5 * x0 + torch.randn(M, N, generator=gen, device="cuda")
+    gamma = (1 + 0.1 * torch.randn(N, generator=gen, device="cuda")).to(dtype)
+    dres0 = torch.randn(M, N, generator=gen, device="cuda") if N % 2 or M == 1100 else None
+    for size in (1e-37, 1e-25, 1e-18, 1e15, 1e17, 1e20, 1e25, 1e30, 1e37):
+        x = (x0.double() * size).to(dtype)
+        at = min(max(size * 1e-20, 1e-10), 1e10)
+        dy = (dy0.double() * at).to(dtype)
+        dres = None if dres0 is None else (dres0.double() * (at / size)).to(dtype)
+        x64 = x.double()
+        mean = x64.mean(1).float() if kind == "ln" else None
+        rstd = 1.0 / (x64 if mean is None else x64 - mean.double()[:, None]).square().mean(1).sqrt()
+        rstd = rstd if kind == "rms64" else rstd.float()
+        (ref, bound), (rdg, bdg), (rdb, bdb) = norm_backward(dy, x, mean, rstd, gamma, dres)
+        dx, dgamma, dbeta = backward(kind, dy, x, mean, rstd, gamma, dres)
+        assert_within(dx, ref, bound + half_ulp(dtype) * (ref.abs() + bound), f"dx at {size}")
+        assert_within(dgamma, rdg, bdg + 8 * U * rdg.abs(), f"dgamma at {size}")
+        if kind == "ln":
+            assert_within(dbeta, rdb, bdb + U * rdb.abs(), f"dbeta at {size}")
