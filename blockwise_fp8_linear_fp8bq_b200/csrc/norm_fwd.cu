@@ -35,8 +35,10 @@ struct FwdParams {
   int tpr;   // threads a row, a multiple of 32
 };
 
+// A variance that rounding left below 0 is 0; one that is NaN (a row with NaN or
+// an infinity) gives NaN.
 __device__ __forceinline__ float rstd_of(float var, float eps) {
-  return __fdiv_rn(1.0f, __fsqrt_rn(fmaxf(var, 0.0f) + eps));
+  return __fdiv_rn(1.0f, __fsqrt_rn((var < 0.0f ? 0.0f : var) + eps));
 }
 
 // A sum over each SUB lanes.

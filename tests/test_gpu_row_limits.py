@@ -79,6 +79,25 @@ def test_table_gradient_of_rows_longer_than_a_grids_second_dimension():
 LAYOUTS = [(1100, 640), (1100, 64), (1100, 100), (1050, 4096), (1100, 641), (40, 2048), (40, 77), (20, 20001)]
 
 
+@pytest.mark.parametrize("M,N", LAYOUTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_layernorm_statistics_of_rows_with_nan_and_infinities(dtype, M, N):
+    """Such a row's rstd is NaN as the definition has it, not that of a row of no
+    variance, its mean is not finite, and the other rows keep their bits."""
+    x = torch.randn(M, N, generator=gen_of(N), device="cuda").to(dtype)
+    clean = fp.layernorm_forward(x)
+    x[3, N - 1] = float("nan")
+    x[7, 0] = float("inf")
+    x[8, N // 2] = -float("inf")
+    x[11, 1], x[11, N - 2] = float("inf"), -float("inf")
+    y, mean, rstd = fp.layernorm_forward(x)
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[[3, 7, 8, 11]] = True
+    assert torch.isnan(rstd[bad]).all() and torch.isnan(y[bad]).all() and not torch.isfinite(mean[bad]).any()
+    for got, want in zip((y, mean, rstd), clean):
+        assert torch.equal(got[~bad], want[~bad])
+
+
 @pytest.mark.parametrize("kind", ["ln", "rms", "rms64"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,N", LAYOUTS + [(1030, 2047), (1100, 2048), (300, 12288)])
