@@ -137,16 +137,26 @@ __device__ __forceinline__ double norm_of(const double* partial, int64_t parts, 
   return sqrt(block_sum(s, red));
 }
 
-// The factor; NaN where the norm is, 1 for an infinite limit.
-__device__ __forceinline__ float factor_of(double norm, double max_norm) {
-  if (isinf(max_norm) && !isnan(norm)) return 1.0f;
+// The factor a * b; NaN where the norm is, 1 for an infinite limit.  b is 1
+// unless the factor is so small (gradients that blew up) that FP32 would hold it
+// with few bits or none although the scaled values are ordinary: then it is the
+// power of two that leaves a all its bits.
+struct Factor {
+  float a, b;
+};
+__device__ __forceinline__ Factor factor_of(double norm, double max_norm) {
+  if (isinf(max_norm) && !isnan(norm)) return Factor{1.0f, 1.0f};
   const double q = max_norm / (norm + 1e-6);
-  return static_cast<float>(q >= 1.0 ? 1.0 : q);
+  if (!(q > 0.0 && q < 0x1p-100)) return Factor{static_cast<float>(q >= 1.0 ? 1.0 : q), 1.0f};
+  int e;
+  frexp(q, &e);
+  e = max(e, -149);
+  return Factor{static_cast<float>(ldexp(q, -e)), static_cast<float>(ldexp(1.0, e))};
 }
 
 // The norm, and the factor for a scaling kernel of many blocks.
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* partial, int64_t parts, double max_norm, float* norm,
-                                                        float* factor) {
+                                                        Factor* factor) {
   __shared__ double red[kThreads / 32];
   cudaGridDependencySynchronize();
   const double r = norm_of(partial, parts, red);
@@ -156,12 +166,16 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* partial, i
 }
 
 template <class T, class O>
-__device__ __forceinline__ void scale_chunk(const T* g, O* out, int n, float f) {
+__device__ __forceinline__ void scale_chunk(const T* g, O* out, int n, Factor f) {
+  if (f.b != 1.0f) {  // rare; a second product in the loops below costs 1-2%
+    for (int i = threadIdx.x; i < n; i += kThreads) out[i] = from_float<O>(to_float(g[i]) * f.a * f.b);
+    return;
+  }
   const int packs = (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) % 16 == 0 ? n / kPack : 0;
   const auto put = [&](const Pack<T, kPack>& v, int i) {
     Pack<O, kPack> o;
 #pragma unroll
-    for (int j = 0; j < kPack; ++j) o.v[j] = from_float<O>(v.f(j) * f);
+    for (int j = 0; j < kPack; ++j) o.v[j] = from_float<O>(v.f(j) * f.a);
     store_pack<true>(out + i * kPack, o);
   };
   if (packs == kUnits * kThreads) {
@@ -178,11 +192,11 @@ __device__ __forceinline__ void scale_chunk(const T* g, O* out, int n, float f) 
     put(v, i);
   }
 #pragma unroll 4
-  for (int i = packs * kPack + threadIdx.x; i < n; i += kThreads) out[i] = from_float<O>(to_float(g[i]) * f);
+  for (int i = packs * kPack + threadIdx.x; i < n; i += kThreads) out[i] = from_float<O>(to_float(g[i]) * f.a);
 }
 
 template <class T, int CAP>
-__device__ __forceinline__ void scale_to(const Table<CAP>& t, int i, int64_t begin, int n, float f) {
+__device__ __forceinline__ void scale_to(const Table<CAP>& t, int i, int64_t begin, int n, Factor f) {
   const T* g = static_cast<const T*>(t.g[i]) + begin;
   switch (t.out_dtype[i]) {
     case FP8BQ_BF16: scale_chunk(g, static_cast<__nv_bfloat16*>(t.out[i]) + begin, n, f); break;
@@ -198,10 +212,10 @@ __device__ __forceinline__ void scale_to(const Table<CAP>& t, int i, int64_t beg
 // of 1 are left alone.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<CAP> t, const double* partial,
-                                                         int64_t parts, double max_norm, float* norm, const float* factor) {
+                                                         int64_t parts, double max_norm, float* norm, const Factor* factor) {
   __shared__ double red[kThreads / 32];
   cudaGridDependencySynchronize();
-  float f;
+  Factor f;
   if (factor != nullptr) {
     f = *factor;
   } else {
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   }
   const int64_t k = t.chunks - 1 - blockIdx.x;
   const int i = tensor_of(t, k);
-  if (f == 1.0f && t.g[i] == t.out[i]) return;
+  if (f.a == 1.0f && f.b == 1.0f && t.g[i] == t.out[i]) return;
   const int64_t begin = (k - t.first[i]) * kChunk;
   const int n = static_cast<int>(min(t.n[i] - begin, static_cast<int64_t>(kChunk)));
   switch (t.in_dtype[i]) {
@@ -251,7 +265,7 @@ cudaError_t run_grad_clip(const fp8bq_grad* grads, int count, double max_norm, b
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  float* factor = static_cast<float*>(workspace);
+  Factor* factor = static_cast<Factor*>(workspace);
   double* partial = static_cast<double*>(workspace) + 2;
   int64_t parts = 0, chunks = 0;
   Table<CAP> t;
@@ -278,7 +292,7 @@ cudaError_t run_grad_clip(const fp8bq_grad* grads, int count, double max_norm, b
     if (t.chunks == 0) break;
     e = launch_dependent(scale_kernel<CAP>, dim3(static_cast<unsigned>(t.chunks)), dim3(kThreads), 0, stream, t,
                          static_cast<const double*>(partial), parts, max_norm, first ? norm : nullptr,
-                         many ? static_cast<const float*>(factor) : nullptr);
+                         many ? static_cast<const Factor*>(factor) : nullptr);
     if (e != cudaSuccess) return e;
     first = false;
   }

@@ -125,3 +125,30 @@ def test_norm_backward_of_tiny_and_huge_rows(M, N, dtype, kind):
         assert_within(dgamma, rdg, bdg + 8 * U * rdg.abs(), f"dgamma at {size}")
         if kind == "ln":
             assert_within(dbeta, rdb, bdb + U * rdb.abs(), f"dbeta at {size}")
+
+
+@pytest.mark.parametrize("most", [1.0, 1e-6, 1e-30, 1e-38])
+@pytest.mark.parametrize("n", [1, 5000, 300001, 6000000])
+def test_clipping_gradients_that_blew_up(n, most):
+    """A limit so far below the norm that their quotient is below FP32's normal
+    range; the clipped values are not."""
+    g = torch.randn(n, generator=gen_of(n), device="cuda").clamp_(-3, 3) * 1e38
+    g64 = g.double()
+    norm = g64.square().sum().sqrt().item()
+    factor = most / (norm + 1e-6)
+    ref = g64 * factor
+    for out in (torch.float32, torch.bfloat16):
+        o = torch.empty(n, dtype=out, device="cuda")
+        fp.clip_grads([g], most, out=[o])
+        # the norm's error, the factor's rounding, the product's, then the type's
+        assert_within(o, ref, (8 * U + half_ulp(out) * (1 + 4 * U)) * ref.abs(), "clipped")
+    over = g.clone()
+    fp.clip_grads([over], most)
+    assert_within(over, ref, (8 * U + half_ulp(torch.float32) * (1 + 4 * U)) * ref.abs(), "clipped in place")
+
+
+def test_a_small_factor_whose_bits_round_to_one_is_not_one():
+    """In place: a factor of 2^-146 (1 - 2^-27) scales, though FP32 rounds its bits up to 1."""
+    g = torch.tensor([2.0 ** 126], device="cuda")
+    fp.clip_grads([g], 2.0 ** -20 * (1 - 2.0 ** -27))
+    assert abs(g.item() - 2.0 ** -20) <= 2.0 ** -20 * 2.0 ** -22
