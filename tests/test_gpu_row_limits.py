@@ -127,6 +127,69 @@ def test_norm_backward_of_tiny_and_huge_rows(M, N, dtype, kind):
             assert_within(dbeta, rdb, bdb + U * rdb.abs(), f"dbeta at {size}")
 
 
+@pytest.mark.parametrize("kind", ["ln", "rms"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", LAYOUTS + [(1500, 2047)])
+def test_dx_over_the_residuals_gradient(M, N, dtype, kind):
+    """The same bits, and the same sums, as into memory of its own."""
+    gen = gen_of(M + N)
+    x = torch.randn(M, N, generator=gen, device="cuda").to(dtype)
+    dy = (torch.randn(M, N, generator=gen, device="cuda") * 0.01).to(dtype)
+    dres = (torch.randn(M, N, generator=gen, device="cuda") * 0.01).to(dtype)
+    mean = x.double().mean(1).float() if kind == "ln" else None
+    rstd = torch.rand(M, generator=gen, device="cuda") + 0.5
+    want = backward(kind, dy, x, mean, rstd, None, dres)
+    over = dres.clone()
+    got = backward(kind, dy, x, mean, rstd, None, over, out=(over, None, None) if kind == "ln" else (over, None))
+    assert got[0] is over or got[0].data_ptr() == over.data_ptr()
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("kind", ["ln", "rms"])
+@pytest.mark.parametrize("M,N", LAYOUTS)
+def test_norm_backward_with_nan_and_infinities(M, N, kind):
+    """They reach dx in their rows alone, dgamma and dbeta in their columns alone."""
+    gen = gen_of(M * 3 + N)
+    x = torch.randn(M, N, generator=gen, device="cuda")
+    dy = torch.randn(M, N, generator=gen, device="cuda") * 0.01
+    mean = x.mean(1) if kind == "ln" else None
+    rstd = torch.rand(M, generator=gen, device="cuda") + 0.5
+    clean = backward(kind, dy, x, mean, rstd)
+    x[3, N - 1] = float("nan")
+    dy[7, 0] = float("nan")
+    dy[11, N // 2] = float("inf")
+    dx, dgamma, dbeta = backward(kind, dy, x, mean, rstd)
+    rows = torch.zeros(M, dtype=torch.bool, device="cuda")
+    rows[[3, 7, 11]] = True
+    assert torch.equal(dx[~rows], clean[0][~rows])
+    assert torch.isnan(dx[3]).all() and torch.isnan(dx[7]).all() and not torch.isfinite(dx[11]).any()
+    cols = torch.zeros(N, dtype=torch.bool, device="cuda")
+    cols[[N - 1, 0, N // 2]] = True
+    assert torch.equal(dgamma[~cols], clean[1][~cols]) and not torch.isfinite(dgamma[cols]).any()
+    if kind == "ln":
+        assert torch.isnan(dbeta[0]) and dbeta[N // 2] == float("inf") and torch.equal(dbeta[1:N // 2], clean[2][1:N // 2])
+
+
+@pytest.mark.parametrize("D", [64, 77])
+@pytest.mark.parametrize("T", [300, 3000])
+def test_table_gradient_with_nan_and_infinities(T, D):
+    """They reach their own token's row; those of tokens that add nothing reach none."""
+    gen = gen_of(T)
+    V = 90
+    ids = torch.randint(1, V - 2, (T,), generator=gen, device="cuda")
+    ids[10], ids[20], ids[30], ids[40] = 0, V, V - 1, V - 2
+    dy = torch.randn(T, D, generator=gen, device="cuda")
+    clean = fp.embedding_backward(dy, ids, V, padding_id=0)
+    dy[10], dy[20] = float("nan"), float("inf")  # padding and an id outside the table
+    dy[30, 3], dy[40, 5] = float("nan"), -float("inf")
+    dw = fp.embedding_backward(dy, ids, V, padding_id=0)
+    assert torch.equal(dw[:V - 2], clean[:V - 2])
+    assert torch.isnan(dw[V - 1, 3]) and dw[V - 1].isnan().sum() == 1
+    assert dw[V - 2, 5] == -float("inf") and (~dw[V - 2].isfinite()).sum() == 1
+    with pytest.raises(fp.Fp8bqError):
+        fp.check()
+
+
 @pytest.mark.parametrize("most", [1.0, 1e-6, 1e-30, 1e-38])
 @pytest.mark.parametrize("n", [1, 5000, 300001, 6000000])
 def test_clipping_gradients_that_blew_up(n, most):
