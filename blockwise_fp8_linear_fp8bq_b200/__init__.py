@@ -637,6 +637,6 @@ def set_clock_counters(counters: Optional[torch.Tensor]) -> None:
 
 def check(stream: Optional[torch.cuda.Stream] = None) -> None:
     """Synchronize and raise if a kernel's bounded wait expired or an embedding call met an id
-    outside its table."""
+    outside its table (after both, this call raises for the wait and the next for the id)."""
     s = stream if stream is not None else torch.cuda.current_stream()
     _raise(lib().fp8bq_check(s.cuda_stream), "fp8bq_check")

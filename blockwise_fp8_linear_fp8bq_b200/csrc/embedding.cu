@@ -11,8 +11,8 @@
 // equal chunks of the sorted tokens are summed run by run, and a run that
 // spans chunks is joined from its chunks' partial sums in order.
 //
-// An id outside [0, V) is never used as an address: it is recorded in the
-// status word, which fp8bq_check() reports, and gives zeros or adds nothing.
+// An id outside [0, V) is never used as an address: it is recorded in the index
+// word, which fp8bq_check() reports, and gives zeros or adds nothing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,7 +34,7 @@ struct LookupParams {
   const void* w;
   const void* ids;
   void* y;
-  int* status;
+  int* index;
   int64_t V, T, ldw, ldy;
   int D, pieces;  // a row is `pieces` pieces of 32 lanes x 4 packs
   float scale;
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) lookup_kernel(const LookupParams p) {
   const int c0 = static_cast<int>(warp - t * p.pieces) * (32 * kPacks * VEC) + lane * VEC;
   const int64_t id = load_id(p.ids, p.i64, t);
   const bool ok = id >= 0 && id < p.V;
-  if (!ok && c0 == 0) atomicCAS(p.status, 0, kStatusIndex);
+  if (!ok && c0 == 0) atomicCAS(p.index, 0, kStatusIndex);
   const W* w = static_cast<const W*>(p.w) + (ok ? id : 0) * p.ldw;
   Y* y = static_cast<Y*>(p.y) + t * p.ldy;
   Pack<W, VEC> v[kPacks];
@@ -114,7 +114,7 @@ struct alignas(8) Token {
 struct SortParams {
   const void* ids;
   Token* buf[2];  // the passes alternate, the last one writes buf[0]
-  int* status;
+  int* index;
   int64_t T, V, padding;
   int64_t per_warp;  // tokens a warp of the cluster owns, a multiple of 32
   int passes, bits;  // digits of `bits` bits
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
       if (pass == 0) {
         const int64_t id = load_id(p.ids, p.i64, i);
         const bool ok = id >= 0 && id < p.V;
-        if (!ok) atomicCAS(p.status, 0, kStatusIndex);
+        if (!ok) atomicCAS(p.index, 0, kStatusIndex);
         k.id = static_cast<uint32_t>(ok && id != p.padding ? id : p.V);
         k.pos = static_cast<uint32_t>(i);
       } else {
@@ -419,7 +419,7 @@ struct FewParams {
   ZeroParams z;
   const void* ids;
   int64_t padding;
-  int* status;
+  int* index;
   bool i64;
 };
 
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(256) grad_few_kernel(const FewParams p) {
   const int t = static_cast<int>(blockIdx.x);
   const int64_t id = load_id(p.ids, p.i64, t);
   if (id < 0 || id >= g.V) {
-    if (tid == 0) atomicCAS(p.status, 0, kStatusIndex);
+    if (tid == 0) atomicCAS(p.index, 0, kStatusIndex);
     return;
   }
   if (id == p.padding) return;
@@ -561,10 +561,10 @@ cudaError_t grad_of_types(const FewParams& f, int dtype, int dw_dtype, bool few,
 }  // namespace
 
 cudaError_t launch_embedding_fwd(const EmbeddingFwd& a, cudaStream_t stream) {
-  int* status = nullptr;
-  const cudaError_t e = device_status_word(&status);
+  int* index = nullptr;
+  const cudaError_t e = device_index_word(&index);
   if (e != cudaSuccess) return e;
-  const LookupParams p{a.w, a.ids, a.y, status, a.V, a.T, a.ldw, a.ldy, static_cast<int>(a.D), 0, a.scale, a.ids_i64};
+  const LookupParams p{a.w, a.ids, a.y, index, a.V, a.T, a.ldw, a.ldy, static_cast<int>(a.D), 0, a.scale, a.ids_i64};
   switch (a.dtype) {
     case FP8BQ_BF16: return lookup_to<__nv_bfloat16>(p, a.out_dtype, stream);
     case FP8BQ_FP16: return lookup_to<__half>(p, a.out_dtype, stream);
@@ -579,8 +579,8 @@ int64_t embedding_bwd_workspace_bytes(int64_t T, int64_t D, int64_t V) {
 }
 
 cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
-  int* status = nullptr;
-  cudaError_t e = device_status_word(&status);
+  int* index = nullptr;
+  cudaError_t e = device_index_word(&index);
   if (e != cudaSuccess) return e;
   const int64_t size = a.dw_dtype == FP8BQ_FP32 ? 4 : 2;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -602,7 +602,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
   if (few_tokens(a.T, a.V, a.D)) {
     f.ids = a.ids;
     f.padding = a.padding;
-    f.status = status;
+    f.index = index;
     f.i64 = a.ids_i64;
     return grad_of_types(f, a.dtype, a.dw_dtype, true, stream);
   }
@@ -610,7 +610,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwd& a, cudaStream_t stream) {
   s.ids = a.ids;
   s.buf[0] = reinterpret_cast<Token*>(ws);
   s.buf[1] = reinterpret_cast<Token*>(ws + tokens_bytes);
-  s.status = status;
+  s.index = index;
   s.T = a.T;
   s.V = a.V;
   s.padding = a.padding;

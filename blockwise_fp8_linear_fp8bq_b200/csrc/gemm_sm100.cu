@@ -1801,7 +1801,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_fused_kernel(const __gr
 }
 
 // ------------------------------------------------------------------- host --
-__device__ int g_device_status;
+__device__ int g_device_status[2];  // the bounded waits' word, and the index word
 
 struct DeviceInfo {
   unsigned long long ctx = 0;  // context the cached addresses and attributes belong to
@@ -2237,6 +2237,12 @@ cudaError_t device_status_word(int** status) {
   return cudaSuccess;
 }
 
+cudaError_t device_index_word(int** index) {
+  const cudaError_t e = device_status_word(index);
+  if (e == cudaSuccess) ++*index;
+  return e;
+}
+
 cudaError_t read_and_clear_device_status(cudaStream_t stream, int* status) {
   *status = 0;
   cudaError_t e = cudaStreamSynchronize(stream);
@@ -2244,15 +2250,16 @@ cudaError_t read_and_clear_device_status(cudaStream_t stream, int* status) {
   DeviceInfo* di = nullptr;
   e = device_info(&di);
   if (e != cudaSuccess) return e;
-  int v = 0;
-  e = cudaMemcpy(&v, di->status, sizeof(int), cudaMemcpyDeviceToHost);
+  int v[2] = {0, 0};
+  e = cudaMemcpy(v, di->status, sizeof(v), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return e;
-  if (v != 0) {
+  const int which = v[0] != 0 ? 0 : 1;
+  if (v[which] != 0) {
     const int zero = 0;
-    e = cudaMemcpy(di->status, &zero, sizeof(int), cudaMemcpyHostToDevice);
+    e = cudaMemcpy(di->status + which, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return e;
   }
-  *status = v;
+  *status = v[which];
   return cudaSuccess;
 }
 

@@ -58,8 +58,9 @@ cudaError_t launch_rmsnorm_quant_exact(const void* x, int64_t M, int64_t K, int6
                                        double eps, double* rstd64, void* h, void* q, void* s_rows, void* qt,
                                        void* s_cols, int fmt, cudaStream_t stream);
 
-// What a kernel records in the device status word for a token id outside its
-// table (the bounded waits record the small codes of their places).
+// What a kernel records in the device's index word for a token id outside its
+// table (the bounded waits record the small codes of their places in the status
+// word).
 constexpr int kStatusIndex = 1000;
 
 // Validated calls of the row operators, in the library's internal form.
@@ -134,6 +135,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 cudaError_t device_sm_count(int* sms);
 // Device address of the kernels' status word on the current device.
 cudaError_t device_status_word(int** status);
+// The same of the word for ids outside their tables: one of its own, so that
+// neither kind of failure hides the other.
+cudaError_t device_index_word(int** index);
 
 // A validated GEMM problem, in the library's internal form.
 struct GemmOperand {
@@ -188,8 +192,8 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t stream, bool* unsuppo
 // (nullptr: stop).
 cudaError_t set_clock_counters(unsigned long long* counters);
 
-// Device status word of the GEMM kernels (0 = ok, else a timeout code).
-// Reads and clears it after synchronizing `stream`.
+// After synchronizing `stream`: the status word (0 = ok, else a timeout code),
+// or where that is 0 the index word.  Clears the one it gives.
 cudaError_t read_and_clear_device_status(cudaStream_t stream, int* status);
 
 }  // namespace fp8bq

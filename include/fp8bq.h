@@ -274,7 +274,7 @@ int fp8bq_rmsnorm_quantize_exact(const void* x, int64_t M, int64_t K, int64_t ld
  *   scale    finite (sqrt(D) in models that scale their embeddings, else 1).
  *   y        [T, D] of out_dtype, leading dimension ldy.
  * An id outside [0, V) reads nothing, gives a row of zeros and is reported
- * as ERR_INDEX by the next fp8bq_check().
+ * as ERR_INDEX by fp8bq_check().
  * Errors: as above; ERR_INVALID_ARG for ids_i64 not 0 or 1 or a scale that is
  * not finite.  T == 0 or D == 0 is a no-op.
  */
@@ -590,11 +590,13 @@ int64_t fp8bq_row_scale_ld(int64_t rows);
 int64_t fp8bq_scales_bytes(int gran, int fmt, int64_t rows, int64_t contraction);
 
 /*
- * Synchronizes `stream`, then reports the first device-side failure since the
- * last check: FP8BQ_ERR_TIMEOUT if a GEMM kernel's bounded wait expired (the
- * kernel then stopped early and its output is undefined), FP8BQ_ERR_INDEX if
- * an embedding call met a token id outside its table, FP8BQ_ERR_CUDA if
- * the stream reported an error.  Clears the recorded state.
+ * Synchronizes `stream`, then reports a device-side failure since the last
+ * check: FP8BQ_ERR_CUDA if the stream reported an error, else
+ * FP8BQ_ERR_TIMEOUT if a bounded wait of a GEMM, a quantizer or a norm expired
+ * (that kernel stopped early and its output is undefined), else
+ * FP8BQ_ERR_INDEX if an embedding call met a token id outside its table.
+ * Clears what it reports; where both of the latter happened, the next check
+ * reports the id.
  */
 int fp8bq_check(fp8bq_stream_t stream);
 
