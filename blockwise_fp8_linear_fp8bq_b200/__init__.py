@@ -553,6 +553,9 @@ def _row_ops():
             from . import _row_binding
         except ImportError as e:
             raise ImportError(f"{e}; build it with `python -m blockwise_fp8_linear_fp8bq_b200.build`") from e
+        if _row_binding.torch_version != torch.__version__:
+            raise ImportError(f"_row_binding.so was built against torch {_row_binding.torch_version}, not "
+                              f"{torch.__version__}; build it with `python -m blockwise_fp8_linear_fp8bq_b200.build`")
         _row_binding.load(_LIB_PATH)
         _rows = _row_binding
     return _rows

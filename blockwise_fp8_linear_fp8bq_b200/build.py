@@ -25,6 +25,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8bq.so")
 BINDING_SRC = os.path.join(CSRC, "row_binding.cpp")
 BINDING = os.path.join(HERE, "_row_binding.so")
+BINDING_TORCH = os.path.join(BUILD, "row_binding.torch")  # the torch that the binding was built against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -58,8 +59,20 @@ def needs_build() -> bool:
     return _older(LIB, _deps()) or needs_binding()
 
 
+def torch_version() -> str:
+    import torch
+    return torch.__version__
+
+
 def needs_binding() -> bool:
-    return _older(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    """Whether the binding is missing, older than its sources, or another torch's."""
+    if _older(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return True
+    try:
+        with open(BINDING_TORCH) as f:
+            return f.read() != torch_version()
+    except FileNotFoundError:
+        return True
 
 
 def build_binding(verbose: bool = False) -> str:
@@ -71,7 +84,8 @@ def build_binding(verbose: bool = False) -> str:
     includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_path("include"), os.path.join(cuda, "include")]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+    version = torch_version()
+    cmd = ["g++", f'-DFP8BQ_TORCH_VERSION="{version}"', "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[a for i in includes for a in ("-isystem" if i != INCLUDE else "-I", i)], BINDING_SRC, "-o", tmp,
            f"-L{libs}", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
     if verbose:
@@ -82,6 +96,9 @@ def build_binding(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed on row_binding.cpp")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_TORCH, "w") as f:
+        f.write(version)
     return BINDING
 
 

@@ -289,6 +289,7 @@ Tensor grads(const std::vector<Tensor>& g, const std::optional<std::vector<Tenso
 }  // namespace
 
 PYBIND11_MODULE(_row_binding, m) {
+  m.attr("torch_version") = FP8BQ_TORCH_VERSION;  // the package refuses the module beside another
   m.def("load", &load);
   m.def("embedding_forward", &embedding_forward);
   m.def("embedding_backward", &embedding_backward);
