@@ -253,10 +253,14 @@ int fp8bq_rmsnorm_quantize_exact(const void* x, int64_t M, int64_t K, int64_t ld
  *   - a dtype is FP8BQ_BF16, FP8BQ_FP16 or FP8BQ_FP32; all arithmetic is FP32
  *     or wider and every output value is rounded once, to nearest even;
  *   - rows of any length and leading dimension, at any address a multiple of
- *     the element size; 16-byte aligned rows whose length is a multiple of 16
- *     bytes are moved 16 bytes at a time, others one element at a time;
- *   - columns past the row length (up to the leading dimension) are neither
- *     read nor written;
+ *     the element size; fastest where every row starts at a multiple of 16
+ *     bytes and is as long as one (others are stored, and read by most calls,
+ *     one or two elements at a time);
+ *   - columns past the row length (up to the leading dimension) enter no
+ *     result and are not written (up to 15 bytes of them beside a row's ends,
+ *     between a tensor's first and last value, may be read);
+ *   - NaN and infinities go where the formulas take them; sums are FP32 (the
+ *     clip's wider) and must stay in its range, as said below;
  *   - sums run in an order fixed by the sizes: equal inputs on equal GPUs
  *     give equal bits;
  *   - a workspace is device memory, 16-byte aligned, of any content; calls
@@ -313,7 +317,10 @@ int64_t fp8bq_embedding_workspace_bytes(int64_t T, int64_t D, int64_t V);
  *   gamma, beta  [N] of param_dtype (dtype or FP8BQ_FP32), or NULL (1 and 0).
  *   eps          finite, >= 0.
  *   mean, rstd   FP32 [M], written (what the backward pass needs), or NULL.
- * Squares of x - mean must not overflow FP32.
+ * A row's sum of x and its sum of (x - mean)^2 must not overflow FP32, nor the
+ * latter vanish where eps is 0: at 2048 columns, deviations up to about 4e17
+ * (beyond, rstd is 0 or NaN).  A row with NaN or an infinity has rstd and y NaN
+ * and a mean that is not finite.
  * Errors: as above; ERR_INVALID_ARG for a bad eps.  M == 0 or N == 0 is a
  * no-op.
  */
@@ -335,13 +342,17 @@ int fp8bq_layernorm_forward(const void* x, int64_t M, int64_t N, int64_t ldx, co
  *   gamma       [N] of param_dtype (dtype or FP8BQ_FP32), or NULL (1).
  *   mean        FP32 [M] (LayerNorm; RMSNorm ignores it).
  *   rstd        FP32 [M], or float64 [M] with FP8BQ_NORM_RSTD_F64 (what
- *               fp8bq_rmsnorm_quantize_exact gives).
+ *               fp8bq_rmsnorm_quantize_exact gives), which is used rounded to
+ *               FP32 and has to lie in its normal range: rows whose root mean
+ *               square is between 3e-39 and 8e37.  rstd^2 may leave it.
  *   dgamma, dbeta  FP32 [N], written, or added to with
  *               FP8BQ_NORM_ACCUMULATE; either may be NULL (RMSNorm ignores
  *               dbeta).
  *   flags       0 or the two above.
  *   workspace   fp8bq_norm_workspace_bytes(M, N) bytes; may be NULL when
  *               that is 0 (few rows) or neither dgamma nor dbeta is wanted.
+ * A row's sums of g and of g * xh, and the columns' sums, must not overflow
+ * FP32.
  * With M == 0, dgamma and dbeta are zeros (or left as they are); N == 0 is a
  * no-op.
  * Errors: as above; ERR_INVALID_ARG for other flag bits or a workspace too
